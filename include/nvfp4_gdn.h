@@ -331,6 +331,92 @@ NVFP4_API nvfp4_status gdn_short_conv(const float* x, int64_t ld_x, int32_t B, i
                                       const float* w, const float* state_in, float* state_out, float* out,
                                       int64_t ld_out, nvfp4_stream_t stream);
 
+/* ----------------------------------------------------- 8-bit operands -- */
+/* The pages compare W4A4 with recipes that hold the GDN projections at 8 bits, keep
+ * the norms unquantised ("Minima" section) and give no formula for either; the calls
+ * of this section are the usual forms of both.
+ *
+ * An E4M3 matrix [rows x cols] with one float32 scale a row: element (r, c) stands
+ * for e4m3(codes[r * ld + c]) * scale[r].  cols % 16 == 0, codes 16-byte aligned,
+ * ld % 16 == 0 (bytes).  A row that held a NaN or an infinity has scale NaN. */
+typedef struct {
+    uint8_t* codes;
+    float* scale; /* [rows] */
+    int64_t rows;
+    int64_t cols;
+    int64_t ld;
+} fp8_tensor;
+
+/* Row-wise E4M3 quantisation of x [rows x cols] (weights, the scan's output):
+ *   S_r = RN(max|x_r| / 448) (1 when max|x_r| < 2^-100), code = E4M3_rn_satfinite(x * RN(1 / S_r)),
+ * float32 operations.  x: device, bf16 or fp32, row pitch ld elements; x and ld *
+ * element size 16-byte aligned.  A row with a NaN or an infinity gets scale NaN and
+ * NaN codes.  out->rows == rows, out->cols == cols; out must not overlap x.
+ * Requirements: 1 <= rows, 16 <= cols <= 32768, cols % 16 == 0. */
+NVFP4_API nvfp4_status fp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld,
+                                    const fp8_tensor* out, nvfp4_stream_t stream);
+
+/* Residual addition, RMS norm and 8-bit quantisation of rows, in one pass:
+ *   h = x + residual              (float32 sum, rounded once to residual's type)
+ *   n = h * w / sqrt(mean(h^2) + eps)
+ *   out = n, quantised row-wise as by fp8_quantize;  norm_bf16 = n rounded to bf16.
+ * The norm is taken of h as it is stored.  Sums and n are float32; n is formed as
+ * RN(RN(h w) rsqrtf(mean + eps)).
+ *   x:        device, bf16 or fp32 (x_dtype), row pitch ld_x elements.
+ *   residual: device, bf16 or fp32, row pitch ld_residual; h: the same type, pitch
+ *             ld_h, written.  h may be residual (same pitch), or x (same type and
+ *             pitch).  Both NULL: h is x and is not written.
+ *   w:        device float32 [cols], 16-byte aligned.   eps: positive, finite.
+ *   out:      NULL, or a host struct of device buffers; norm_bf16: NULL, or device
+ *             bf16 with row pitch ld_norm; at least one of the two.  Neither may
+ *             overlap anything else.
+ *   amax_word (device, nullable; needs norm_bf16): the maximum |norm_bf16| is folded
+ *             into it with atomicMax on the float bits (it must hold a non-negative
+ *             float, e.g. 0, beforehand).  As word 0 of nvfp4_quantize's workspace it
+ *             lets NVFP4_QUANT_FROM_AMAX quantise norm_bf16 in one pass.
+ * Matrices and pitches (times the element size) are 16-byte aligned.  A row whose mean
+ * square, or whose largest |h w / sqrt(..)|, is not a finite float32 gets NaN
+ * throughout.  Requirements as for fp8_quantize. */
+NVFP4_API nvfp4_status add_rmsnorm_quantize(const void* x, int32_t x_dtype, int64_t ld_x, const void* residual,
+                                            int32_t residual_dtype, int64_t ld_residual, const float* w, float eps,
+                                            int64_t rows, int64_t cols, void* h, int64_t ld_h, const fp8_tensor* out,
+                                            void* norm_bf16, int64_t ld_norm, unsigned int* amax_word,
+                                            nvfp4_stream_t stream);
+
+/* ------------------------------------------------------- fused epilogues -- */
+enum { GEMM_ACT_NONE = 0, GEMM_ACT_SILU = 1, GEMM_ACT_GELU = 2, GEMM_ACT_RELU = 3 };
+
+/* What happens to a product p[m, n] before it is stored, all in float32 with one
+ * rounding at the end:  out[m, n] = act(p[m, n] + bias[n]) + residual[m, n].
+ *   act:      SILU x / (1 + exp(-x));  GELU x (1 + erf(x / sqrt 2)) / 2;  RELU max(x, 0).
+ *   residual: may be out itself, with the same type and pitch (the residual stream is
+ *             then updated in place); any other overlap is not allowed.
+ * Pointers need the alignment of their element type only; N and the pitches are free
+ * (ldc, ld_residual >= N).  Host struct of device pointers. */
+typedef struct {
+    const float* bias;    /* float32 [N], or NULL */
+    int32_t act;          /* GEMM_ACT_* */
+    const void* residual; /* bf16 or fp32 [M x N], or NULL */
+    int32_t residual_dtype;
+    int64_t ld_residual;
+    void* out;            /* bf16 or fp32 [M x N] */
+    int32_t out_dtype;
+    int64_t ldc;
+} gemm_epilogue;
+
+/* p[m, n] = A->scale[m] B->scale[n] sum_k e4m3(A)[m, k] e4m3(B)[n, k], tensor-core
+ * products accumulated in float32 (tcgen05 kind::f8f6f4), then the epilogue.
+ * A: [M x K] (activations), B: [N x K] (weights).  The result does not depend on
+ * timing: no atomics, a fixed order of summation for given sizes.
+ * Requirements: K % 16 == 0, A->cols == B->cols == K <= 2^24, M, N <= 2^30. */
+NVFP4_API nvfp4_status w8a8_gemm(const fp8_tensor* A, const fp8_tensor* B, const gemm_epilogue* epilogue,
+                                 nvfp4_stream_t stream);
+
+/* w4a4_gemm's product (NVFP4 operands, see there) with the epilogue above.
+ * Requirements: K % 64 == 0, A->cols == B->cols == K, M, N <= 2^30. */
+NVFP4_API nvfp4_status w4a4_gemm_fused(const nvfp4_tensor* A, const nvfp4_tensor* B, const gemm_epilogue* epilogue,
+                                       nvfp4_stream_t stream);
+
 /* ---------------------------------------------------------------- layer -- */
 typedef struct {
     nvfp4_tensor w_in;    /* [N_in x hidden], N_in = 2*Hk*K + 2*Hv*V + 2*Hv, one global scale */

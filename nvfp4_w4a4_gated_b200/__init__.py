@@ -25,12 +25,15 @@ __all__ = [
     "selftest_wait_timeout", "FORM_PAGES",
     "FORM_STANDARD", "SCAN_AUTO", "SCAN_RECURRENT", "SCAN_CHUNKED", "EXPORTED_SYMBOLS", "QUANT_COMPUTE_SCALE",
     "QUANT_GIVEN_SCALE", "QUANT_AMAX_ONLY", "QUANT_FROM_AMAX",
+    "FP8Matrix", "fp8_quantize", "add_rmsnorm_quantize", "w8a8_gemm", "w4a4_gemm_fused", "ACT_NONE", "ACT_SILU",
+    "ACT_GELU", "ACT_RELU",
 ]
 
 FORM_PAGES, FORM_STANDARD = 0, 1
 SCAN_AUTO, SCAN_RECURRENT, SCAN_CHUNKED = 0, 1, 2
 DTYPE_BF16, DTYPE_FP32 = 0, 1
 QUANT_COMPUTE_SCALE, QUANT_GIVEN_SCALE, QUANT_AMAX_ONLY, QUANT_FROM_AMAX = 0, 1, 2, 3
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_RELU = 0, 1, 2, 3
 
 STATUS = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED_SHAPE", 3: "MISALIGNED", 4: "CUDA", 5: "TIMEOUT", 6: "WORKSPACE"}
 
@@ -40,7 +43,7 @@ EXPORTED_SYMBOLS = [
     "gdn_scan", "gdn_layer_workspace_layout", "gdn_layer_forward", "gdn_scan_noalloc", "gdn_output_gate",
     "gdn_short_conv", "gdn_layer_forward_stateful", "gdn_scan_transition_workspace_size", "gdn_scan_transition",
     "gdn_state_combine", "gdn_scan_correct", "gdn_scan_span_workspace_size", "gdn_scan_span",
-    "gdn_layer_forward_timed",
+    "gdn_layer_forward_timed", "fp8_quantize", "add_rmsnorm_quantize", "w8a8_gemm", "w4a4_gemm_fused",
 ]
 
 
@@ -88,6 +91,17 @@ class _Layout(ctypes.Structure):
     _fields_ = [(f, ctypes.c_size_t) for f in _LAYOUT_FIELDS]
 
 
+class _Fp8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("ld", ctypes.c_int64)]
+
+
+class _Epilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("act", ctypes.c_int32), ("residual", ctypes.c_void_p),
+                ("residual_dtype", ctypes.c_int32), ("ld_residual", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_dtype", ctypes.c_int32), ("ldc", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -132,8 +146,15 @@ def lib() -> ctypes.CDLL:
         L.gdn_scan_span_workspace_size.restype = sz
         L.gdn_scan_span.argtypes = [P, P, P, i64, P, P, i32, i64, DP, ctypes.c_float, i32, i32, P, P, P, P, P, sz, P]
         L.gdn_scan_correct.argtypes = [P, P, P, i32, i64, i32, i32, i32, P, P]
+        FP, EP = ctypes.POINTER(_Fp8), ctypes.POINTER(_Epilogue)
+        L.fp8_quantize.argtypes = [P, i32, i64, i64, i64, FP, P]
+        L.add_rmsnorm_quantize.argtypes = [P, i32, i64, P, i32, i64, P, ctypes.c_float, i64, i64, P, i64, FP, P, i64, P,
+                                           P]
+        L.w8a8_gemm.argtypes = [FP, FP, EP, P]
+        L.w4a4_gemm_fused.argtypes = [TP, TP, EP, P]
         for f in ("nvfp4_check_device_error", "nvfp4_selftest_wait_timeout", "nvfp4_quantize", "w4a4_gemm", "gdn_gates", "gdn_scan",
-                  "gdn_layer_workspace_layout", "gdn_layer_forward", "gdn_scan_noalloc", "gdn_layer_forward_timed"):
+                  "gdn_layer_workspace_layout", "gdn_layer_forward", "gdn_scan_noalloc", "gdn_layer_forward_timed",
+                  "fp8_quantize", "add_rmsnorm_quantize", "w8a8_gemm", "w4a4_gemm_fused"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -164,6 +185,43 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+
+
+def _want(t, name: str, *dtypes, shape=None, device=None):
+    """A CUDA matrix with contiguous rows, of one of ``dtypes`` (and of ``shape``, on ``device``)."""
+    _dev_addr(t)
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name}: a matrix with contiguous rows is expected")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _want_vector(t, name: str, n: int, device):
+    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: {n} contiguous float32 values are expected")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _pitch(t) -> int:
+    """Row pitch in elements; a single row's stride says nothing."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _on(device, stream, call, *args):
+    """Run a library call with ``device`` current, on ``stream`` or that device's current one."""
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            _check(call(*args, _stream(stream)))
+    else:
+        _check(call(*args, _stream(stream)))
+
+
 # ------------------------------------------------------------------ tensors --
 @dataclasses.dataclass
 class NVFP4Matrix:
@@ -183,6 +241,24 @@ class NVFP4Matrix:
 
     def c(self) -> _Tensor:
         return _Tensor(_dev_addr(self.codes), _dev_addr(self.sf), _dev_addr(self.scale), self.rows, self.cols)
+
+
+@dataclasses.dataclass
+class FP8Matrix:
+    """Device buffers of an E4M3 matrix with one scale a row: codes * scale[:, None]."""
+    codes: torch.Tensor      # float8_e4m3fn [rows, cols], rows codes.stride(0) bytes apart
+    scale: torch.Tensor      # float32 [rows]
+
+    @staticmethod
+    def empty(rows: int, cols: int, device="cuda") -> "FP8Matrix":
+        return FP8Matrix(torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device),
+                         torch.empty(rows, dtype=torch.float32, device=device))
+
+    def c(self) -> _Fp8:
+        _want(self.codes, "codes", torch.float8_e4m3fn)
+        rows, cols = self.codes.shape
+        _want_vector(self.scale, "scale", rows, self.codes.device)
+        return _Fp8(self.codes.data_ptr(), self.scale.data_ptr(), rows, cols, _pitch(self.codes))
 
 
 @dataclasses.dataclass(frozen=True)
@@ -270,6 +346,104 @@ def w4a4_gemm(A: NVFP4Matrix, B: NVFP4Matrix, C: torch.Tensor | None = None, str
     ta, tb = A.c(), B.c()
     _check(lib().w4a4_gemm(ctypes.byref(ta), ctypes.byref(tb), _ptr(C), C.stride(0), _stream(stream)))
     return C
+
+
+def fp8_quantize(x: torch.Tensor, out: FP8Matrix | None = None, stream=None) -> FP8Matrix:
+    """Quantise the rows of a bf16 or fp32 CUDA matrix to E4M3 codes with one scale a row."""
+    _want(x, "x", torch.bfloat16, torch.float32)
+    rows, cols = x.shape
+    if out is None:
+        out = FP8Matrix.empty(rows, cols, x.device)
+    else:
+        _want(out.codes, "out", torch.float8_e4m3fn, shape=x.shape, device=x.device)
+    q = out.c()
+    _on(x.device, stream, lib().fp8_quantize, x.data_ptr(), _DTYPES[x.dtype], rows, cols, _pitch(x), ctypes.byref(q))
+    return out
+
+
+def add_rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                         h=None, out: FP8Matrix | None = None, want_fp8: bool = True, norm=None,
+                         want_norm: bool = False, amax_word=None, stream=None):
+    """h = x + residual, n = h * w / sqrt(mean(h^2) + eps) per row, n quantised to
+    E4M3 with one scale a row.  Returns (h, FP8Matrix, n): h has residual's type (a new
+    tensor unless given; may be residual; x itself without a residual), the FP8Matrix
+    is None with want_fp8=False, n (bf16) is None unless want_norm or ``norm`` is given.
+    amax_word (uint32 word on the device) takes the maximum |n| of the bf16 n."""
+    _want(x, "x", torch.bfloat16, torch.float32)
+    rows, cols = x.shape
+    dev = x.device
+    _want_vector(w, "w", cols, dev)
+    r_ptr, r_dtype, r_ld, h_ptr, h_ld = None, 0, 0, None, 0
+    if residual is not None:
+        _want(residual, "residual", torch.bfloat16, torch.float32, shape=x.shape, device=dev)
+        if h is None:
+            h = torch.empty((rows, cols), dtype=residual.dtype, device=dev)
+        else:
+            _want(h, "h", residual.dtype, shape=x.shape, device=dev)
+        r_ptr, r_dtype, r_ld = residual.data_ptr(), _DTYPES[residual.dtype], _pitch(residual)
+        h_ptr, h_ld = h.data_ptr(), _pitch(h)
+    elif h is not None:
+        raise ValueError("h is written only with a residual")
+    q = None
+    if out is not None or want_fp8:
+        if out is None:
+            out = FP8Matrix.empty(rows, cols, dev)
+        else:
+            _want(out.codes, "out", torch.float8_e4m3fn, shape=x.shape, device=dev)
+        q = ctypes.byref(out.c())
+    if norm is None and want_norm:
+        norm = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    elif norm is not None:
+        _want(norm, "norm", torch.bfloat16, shape=x.shape, device=dev)
+    if amax_word is not None and (amax_word.device != dev or amax_word.element_size() != 4 or amax_word.numel() < 1):
+        raise ValueError("amax_word: a 32-bit word on x's device is expected")
+    _on(dev, stream, lib().add_rmsnorm_quantize, x.data_ptr(), _DTYPES[x.dtype], _pitch(x), r_ptr, r_dtype, r_ld,
+        w.data_ptr(), float(eps), rows, cols, h_ptr, h_ld, q, None if norm is None else norm.data_ptr(),
+        0 if norm is None else _pitch(norm), None if amax_word is None else amax_word.data_ptr())
+    return (x if residual is None else h), out, norm
+
+
+def _epilogue(M: int, N: int, dev, bias, act: int, residual, out, out_dtype):
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    else:
+        _want(out, "out", torch.bfloat16, torch.float32, shape=(M, N), device=dev)
+    if out.dtype not in _DTYPES:
+        raise ValueError(f"out_dtype {out.dtype}: bfloat16 or float32 is expected")
+    if bias is not None:
+        _want_vector(bias, "bias", N, dev)
+    r_ptr, r_dtype, r_ld = None, 0, 0
+    if residual is not None:
+        _want(residual, "residual", torch.bfloat16, torch.float32, shape=(M, N), device=dev)
+        r_ptr, r_dtype, r_ld = residual.data_ptr(), _DTYPES[residual.dtype], _pitch(residual)
+    return out, _Epilogue(None if bias is None else bias.data_ptr(), act, r_ptr, r_dtype, r_ld, out.data_ptr(),
+                          _DTYPES[out.dtype], _pitch(out))
+
+
+def w8a8_gemm(A: FP8Matrix, B: FP8Matrix, bias=None, act: int = ACT_NONE, residual=None, out=None,
+              out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """act(A @ B^T + bias) + residual for E4M3 operands with row scales: A [M, K]
+    activations, B [N, K] weights, bias float32 [N], residual bf16 or fp32 [M, N].
+    out (bf16 or fp32 [M, N]; a new tensor of out_dtype unless given) may be residual."""
+    a, b = A.c(), B.c()
+    dev = A.codes.device
+    if B.codes.device != dev:
+        raise ValueError(f"B is on {B.codes.device}, A on {dev}")
+    out, e = _epilogue(a.rows, b.rows, dev, bias, act, residual, out, out_dtype)
+    _on(dev, stream, lib().w8a8_gemm, ctypes.byref(a), ctypes.byref(b), ctypes.byref(e))
+    return out
+
+
+def w4a4_gemm_fused(A: NVFP4Matrix, B: NVFP4Matrix, bias=None, act: int = ACT_NONE, residual=None, out=None,
+                    out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """act(A @ B^T + bias) + residual for NVFP4 operands; arguments as for w8a8_gemm."""
+    a, b = A.c(), B.c()
+    dev = A.codes.device
+    if B.codes.device != dev:
+        raise ValueError(f"B is on {B.codes.device}, A on {dev}")
+    out, e = _epilogue(A.rows, B.rows, dev, bias, act, residual, out, out_dtype)
+    _on(dev, stream, lib().w4a4_gemm_fused, ctypes.byref(a), ctypes.byref(b), ctypes.byref(e))
+    return out
 
 
 def gdn_gates(proj: torch.Tensor, dims: GdnDims, A_log: torch.Tensor, dt_bias: torch.Tensor, stream=None):

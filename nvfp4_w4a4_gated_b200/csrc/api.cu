@@ -69,12 +69,12 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-nvfp4_status make_tmap_u8_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes,
-                                uint32_t box_rows, uint32_t box_bytes) {
+nvfp4_status make_tmap_u8_sw128_ld(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes, uint64_t ld,
+                                   uint32_t box_rows, uint32_t box_bytes) {
     auto fn = encode_fn();
     if (!fn) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
     cuuint64_t dims[2] = {row_bytes, rows};
-    cuuint64_t strides[1] = {row_bytes};
+    cuuint64_t strides[1] = {ld};
     cuuint32_t box[2] = {box_bytes, box_rows};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
@@ -82,6 +82,11 @@ nvfp4_status make_tmap_u8_sw128(CUtensorMap* map, const void* base, uint64_t row
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string(r));
     return NVFP4_OK;
+}
+
+nvfp4_status make_tmap_u8_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes,
+                                uint32_t box_rows, uint32_t box_bytes) {
+    return make_tmap_u8_sw128_ld(map, base, rows, row_bytes, row_bytes, box_rows, box_bytes);
 }
 
 nvfp4_status make_tmap_f32_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld,

@@ -65,6 +65,9 @@ nvfp4_status smem_limit_once(PerDeviceOnce& once, Kern kernel, int bytes, const 
 // (row pitch = row_bytes) with a box of box_rows x box_bytes and 128-byte swizzle.
 nvfp4_status make_tmap_u8_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes,
                                 uint32_t box_rows, uint32_t box_bytes);
+// The same over rows of row_bytes bytes, ld bytes apart (ld % 16 == 0).
+nvfp4_status make_tmap_u8_sw128_ld(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes, uint64_t ld,
+                                   uint32_t box_rows, uint32_t box_bytes);
 
 // 2-D tiled TMA descriptor over a row-major float32 matrix [rows x cols] with
 // row pitch ld elements, box box_rows x box_cols (box_cols * 4 <= 128), 128-byte swizzle.

@@ -1,0 +1,110 @@
+"""What the block operators refuse, on the host and before any launch (CPU only: no
+call here reaches a kernel)."""
+import ctypes
+
+import pytest
+import torch
+
+import nvfp4_w4a4_gated_b200 as nv
+
+FAKE = 0x10000  # a 16-byte aligned non-null address; never dereferenced (validation fails first)
+BF16, FP32 = nv.DTYPE_BF16, nv.DTYPE_FP32
+
+
+def fp8(rows=128, cols=256, ld=None, codes=FAKE, scale=FAKE):
+    return nv._Fp8(codes, scale, rows, cols, cols if ld is None else ld)
+
+
+def quantize(x=FAKE, dtype=BF16, rows=128, cols=256, ld=None, out=None):
+    t = out if out is not None else fp8(rows, cols)
+    return nv.lib().fp8_quantize(x, dtype, rows, cols, cols if ld is None else ld, ctypes.byref(t), None)
+
+
+@pytest.mark.parametrize("status,kw", [
+    (1, dict(x=None)), (1, dict(dtype=7)), (1, dict(rows=0)), (1, dict(cols=0)), (2, dict(cols=24)),
+    (2, dict(cols=32768 + 16)), (2, dict(rows=1 << 31)), (1, dict(ld=240)), (3, dict(x=FAKE + 2)), (3, dict(ld=260)),
+    (1, dict(out=fp8(128, 272))), (1, dict(out=fp8(127, 256))), (1, dict(out=fp8(codes=0))), (1, dict(out=fp8(scale=0))),
+    (3, dict(out=fp8(codes=FAKE + 8))), (3, dict(out=fp8(ld=264))), (1, dict(out=fp8(ld=240))), (3, dict(out=fp8(scale=FAKE + 2))),
+])
+def test_quantize(status, kw):
+    assert quantize(**kw) == status
+    assert nv.lib().nvfp4_last_error()
+
+
+def norm(x=FAKE, xt=FP32, ld_x=256, r=FAKE, rt=BF16, ld_r=256, w=FAKE, eps=1e-6, rows=128, cols=256, h=FAKE, ld_h=256,
+         out=True, n=None, ld_n=256, amax=None):
+    t = fp8(rows, cols) if out is True else out
+    return nv.lib().add_rmsnorm_quantize(x, xt, ld_x, r, rt, ld_r, w, eps, rows, cols, h, ld_h,
+                                         None if t is None else ctypes.byref(t), n, ld_n, amax, None)
+
+
+@pytest.mark.parametrize("status,kw", [
+    (1, dict(x=None)), (1, dict(w=None)), (1, dict(xt=9)), (1, dict(rt=-1)), (1, dict(eps=0.0)), (1, dict(eps=-1.0)),
+    (1, dict(eps=float("nan"))), (1, dict(eps=float("inf"))), (1, dict(rows=0)), (1, dict(cols=0)), (2, dict(cols=40)),
+    (2, dict(cols=65536, ld_x=65536)), (1, dict(h=None)), (1, dict(r=None)), (1, dict(out=None)), (1, dict(amax=FAKE)),
+    (1, dict(ld_x=248)), (1, dict(ld_r=240)), (1, dict(ld_h=240)), (1, dict(n=FAKE, ld_n=240)), (3, dict(x=FAKE + 4)),
+    (3, dict(ld_x=258)), (3, dict(r=FAKE + 2)), (3, dict(ld_r=260)), (3, dict(h=FAKE + 8)), (3, dict(w=FAKE + 4)),
+    (3, dict(n=FAKE + 2)), (3, dict(n=FAKE, ld_n=260)), (1, dict(out=fp8(128, 240))), (3, dict(out=fp8(codes=FAKE + 4))),
+])
+def test_norm(status, kw):
+    assert norm(**kw) == status
+    assert nv.lib().nvfp4_last_error()
+
+
+def epilogue(bias=None, act=0, r=None, rt=BF16, ld_r=64, out=FAKE, ot=BF16, ldc=64):
+    return nv._Epilogue(bias, act, r, rt, ld_r, out, ot, ldc)
+
+
+EPILOGUES = [
+    (1, dict(out=None)), (1, dict(ot=3)), (1, dict(act=-1)), (1, dict(act=4)), (1, dict(ldc=63)), (3, dict(out=FAKE + 1)),
+    (3, dict(out=FAKE + 2, ot=FP32)), (3, dict(bias=FAKE + 2)), (1, dict(r=FAKE + 64, rt=5)), (1, dict(r=FAKE + 64, ld_r=63)),
+    (3, dict(r=FAKE + 1)), (3, dict(r=FAKE + 2, rt=FP32)), (1, dict(r=FAKE, rt=FP32)), (1, dict(r=FAKE, ld_r=65)),
+]
+
+
+@pytest.mark.parametrize("status,kw", EPILOGUES)
+def test_w8a8_epilogue(status, kw):
+    A, B, e = fp8(8, 256), fp8(64, 256), epilogue(**kw)
+    assert nv.lib().w8a8_gemm(ctypes.byref(A), ctypes.byref(B), ctypes.byref(e), None) == status
+
+
+@pytest.mark.parametrize("status,kw", EPILOGUES)
+def test_w4a4_epilogue(status, kw):
+    A, B, e = (nv._Tensor(FAKE, FAKE, FAKE, rows, 256) for rows in (8, 64)), None, epilogue(**kw)
+    A, B = tuple(A)
+    assert nv.lib().w4a4_gemm_fused(ctypes.byref(A), ctypes.byref(B), ctypes.byref(e), None) == status
+
+
+@pytest.mark.parametrize("status,a,b", [
+    (1, fp8(8, 256), fp8(64, 272)), (1, fp8(0, 256), fp8(64, 256)), (2, fp8(8, 24), fp8(64, 24)),
+    (1, fp8(8, 256, ld=240), fp8(64, 256)), (3, fp8(8, 256, codes=FAKE + 8), fp8(64, 256)),
+    (3, fp8(8, 256), fp8(64, 256, ld=264)), (1, fp8(8, 256, scale=0), fp8(64, 256)), (1, fp8(8, 256), fp8(64, 256, codes=0)),
+    (2, fp8(1 << 31, 256), fp8(64, 256)), (2, fp8((1 << 30) + 1, 256), fp8(64, 256)), (2, fp8(8, (1 << 24) + 16), fp8(64, (1 << 24) + 16)),
+])
+def test_w8a8_operands(status, a, b):
+    e = epilogue()
+    assert nv.lib().w8a8_gemm(ctypes.byref(a), ctypes.byref(b), ctypes.byref(e), None) == status
+    assert nv.lib().nvfp4_last_error()
+
+
+def test_null_structs():
+    L, A, e = nv.lib(), fp8(64, 256), epilogue()
+    assert L.w8a8_gemm(None, ctypes.byref(A), ctypes.byref(e), None) == 1
+    assert L.w8a8_gemm(ctypes.byref(A), None, ctypes.byref(e), None) == 1
+    assert L.w8a8_gemm(ctypes.byref(A), ctypes.byref(A), None, None) == 1
+    assert L.fp8_quantize(FAKE, BF16, 64, 256, 256, None, None) == 1
+
+
+def test_w4a4_operands():
+    e = epilogue()
+    for status, a, b in ((1, (8, 256), (64, 320)), (2, (8, 96), (64, 96)), (2, ((1 << 30) + 1, 256), (64, 256))):
+        A, B = (nv._Tensor(FAKE, FAKE, FAKE, *t) for t in (a, b))
+        assert nv.lib().w4a4_gemm_fused(ctypes.byref(A), ctypes.byref(B), ctypes.byref(e), None) == status
+
+
+def test_host_tensors_are_refused():
+    x, w = torch.zeros(4, 64), torch.ones(64)
+    q = nv.FP8Matrix(torch.zeros(4, 64).to(torch.float8_e4m3fn), torch.ones(4))
+    for call in (lambda: nv.fp8_quantize(x), lambda: nv.add_rmsnorm_quantize(x, w), lambda: nv.w8a8_gemm(q, q)):
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            call()
