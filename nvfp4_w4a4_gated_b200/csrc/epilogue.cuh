@@ -25,6 +25,21 @@ struct EpiArgs {
     int M, N;
 };
 
+// One column of C: token m0 + j of row pitch ld, this thread's n.  A whole chunk runs
+// without a test per token (each test is a branch, and a branch per element keeps the
+// accesses from being in flight together); only the last tokens' chunk tests.
+template <int C, typename F>
+__device__ __forceinline__ void for_tokens(int m0, int M, F f) {
+    if (m0 + C <= M) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) f(j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+            if (m0 + j < M) f(j);
+    }
+}
+
 // R[m0 + j, n] for j < C (0 where there is none).  R may be C itself: a thread reads
 // each element before it, and nobody else, writes it, so these are plain loads.
 template <int C>
@@ -35,14 +50,10 @@ __device__ __forceinline__ void epilogue_residual(const EpiArgs& e, int m0, int 
     const int64_t at = m0 * e.ld_res + n;
     if (e.res_dtype == NVFP4_DTYPE_BF16) {
         const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(e.res) + at;
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-            if (m0 + j < e.M) r[j] = __bfloat162float(p[j * e.ld_res]);
+        for_tokens<C>(m0, e.M, [&](int j) { r[j] = __bfloat162float(p[j * e.ld_res]); });
     } else {
         const float* p = static_cast<const float*>(e.res) + at;
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-            if (m0 + j < e.M) r[j] = p[j * e.ld_res];
+        for_tokens<C>(m0, e.M, [&](int j) { r[j] = p[j * e.ld_res]; });
     }
 }
 
@@ -65,14 +76,10 @@ __device__ __forceinline__ void epilogue_store(const EpiArgs& e, int m0, int n, 
     const int64_t at = m0 * e.ldc + n;
     if (e.out_dtype == NVFP4_DTYPE_BF16) {
         __nv_bfloat16* p = static_cast<__nv_bfloat16*>(e.out) + at;
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-            if (m0 + j < e.M) p[j * e.ldc] = __float2bfloat16_rn(v[j] + r[j]);
+        for_tokens<C>(m0, e.M, [&](int j) { p[j * e.ldc] = __float2bfloat16_rn(v[j] + r[j]); });
     } else {
         float* p = static_cast<float*>(e.out) + at;
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-            if (m0 + j < e.M) p[j * e.ldc] = v[j] + r[j];
+        for_tokens<C>(m0, e.M, [&](int j) { p[j * e.ldc] = v[j] + r[j]; });
     }
 }
 

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(320, 1)
     pdl_wait_and_trigger();
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             // ---------------------------------------------------- producer --
             uint32_t stage = 0, phase = 0;
             for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
@@ -203,7 +203,9 @@ __global__ void __launch_bounds__(320, 1)
         producer_done:;
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        // elect.sync, not `lane == 0`: the compiler then knows that one lane runs the role
+        // and issues each MMA straight from uniform registers
+        if (elect_one()) {
             // --------------------------------------------------------- MMA --
             uint32_t stage = 0, phase = 0, kt_all = 0;
             int local = 0;
