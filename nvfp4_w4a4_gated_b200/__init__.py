@@ -186,40 +186,57 @@ def _stream(stream):
 
 
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+_FP8 = {torch.float8_e4m3fn: 0}
+
+# The block operators' small calls last a few microseconds on the device, so their
+# wrappers read each tensor once and ask torch for the stream's handle alone.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _want(t, name: str, *dtypes, shape=None, device=None):
-    """A CUDA matrix with contiguous rows, of one of ``dtypes`` (and of ``shape``, on ``device``)."""
-    _dev_addr(t)
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+def _rows(t, name: str, dtypes=_DTYPES, shape=None, dev=None):
+    """(address, rows, cols, row pitch in elements, dtype code, device index) of a CUDA
+    matrix with contiguous rows; its dtype in ``dtypes``, its shape and device as given."""
+    at = t.get_device()
+    code = dtypes.get(t.dtype)
+    sh, st = t.shape, t.stride()
+    if at < 0:
+        _dev_addr(t)
+    if code is None:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {list(dtypes)}")
+    if len(sh) != 2 or (st[1] != 1 and sh[1] > 1):
         raise ValueError(f"{name}: a matrix with contiguous rows is expected")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if shape is not None and sh != shape:
+        raise ValueError(f"{name}: shape {tuple(sh)}, expected {tuple(shape)}")
+    if dev is not None and at != dev:
+        raise ValueError(f"{name} is on cuda:{at}, expected cuda:{dev}")
+    rows, cols = sh
+    return t.data_ptr(), rows, cols, st[0] if rows > 1 else cols, code, at   # one row: its stride says nothing
 
 
-def _want_vector(t, name: str, n: int, device):
+def _vector(t, name: str, n: int, dev: int) -> int:
+    """Address of n contiguous float32 values on device ``dev``."""
     if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: {n} contiguous float32 values are expected")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    return t.data_ptr()
 
 
-def _pitch(t) -> int:
-    """Row pitch in elements; a single row's stride says nothing."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _on(device, stream, call, *args):
-    """Run a library call with ``device`` current, on ``stream`` or that device's current one."""
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            _check(call(*args, _stream(stream)))
+def _on(dev: int, stream, call, *args):
+    """A library call with device ``dev`` current, on ``stream`` or that device's current one."""
+    if stream is None:
+        handle = _raw_stream(dev)
     else:
-        _check(call(*args, _stream(stream)))
+        if stream.device_index != dev:
+            raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            status = call(*args, handle)
+    else:
+        status = call(*args, handle)
+    if status:
+        _check(status)
 
 
 # ------------------------------------------------------------------ tensors --
@@ -254,11 +271,9 @@ class FP8Matrix:
         return FP8Matrix(torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device),
                          torch.empty(rows, dtype=torch.float32, device=device))
 
-    def c(self) -> _Fp8:
-        _want(self.codes, "codes", torch.float8_e4m3fn)
-        rows, cols = self.codes.shape
-        _want_vector(self.scale, "scale", rows, self.codes.device)
-        return _Fp8(self.codes.data_ptr(), self.scale.data_ptr(), rows, cols, _pitch(self.codes))
+    def c(self, shape=None, dev=None) -> _Fp8:
+        ptr, rows, cols, ld, _, at = _rows(self.codes, "codes", _FP8, shape, dev)
+        return _Fp8(ptr, _vector(self.scale, "scale", rows, at), rows, cols, ld)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -348,16 +363,17 @@ def w4a4_gemm(A: NVFP4Matrix, B: NVFP4Matrix, C: torch.Tensor | None = None, str
     return C
 
 
+def _fp8_like(x, rows: int) -> FP8Matrix:
+    return FP8Matrix(torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format),
+                     x.new_empty(rows, dtype=torch.float32))
+
+
 def fp8_quantize(x: torch.Tensor, out: FP8Matrix | None = None, stream=None) -> FP8Matrix:
     """Quantise the rows of a bf16 or fp32 CUDA matrix to E4M3 codes with one scale a row."""
-    _want(x, "x", torch.bfloat16, torch.float32)
-    rows, cols = x.shape
+    ptr, rows, cols, ld, dtype, dev = _rows(x, "x")
     if out is None:
-        out = FP8Matrix.empty(rows, cols, x.device)
-    else:
-        _want(out.codes, "out", torch.float8_e4m3fn, shape=x.shape, device=x.device)
-    q = out.c()
-    _on(x.device, stream, lib().fp8_quantize, x.data_ptr(), _DTYPES[x.dtype], rows, cols, _pitch(x), ctypes.byref(q))
+        out = _fp8_like(x, rows)
+    _on(dev, stream, lib().fp8_quantize, ptr, dtype, rows, cols, ld, ctypes.byref(out.c(x.shape, dev)))
     return out
 
 
@@ -368,56 +384,49 @@ def add_rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, residual: torch.Tenso
     E4M3 with one scale a row.  Returns (h, FP8Matrix, n): h has residual's type (a new
     tensor unless given; may be residual; x itself without a residual), the FP8Matrix
     is None with want_fp8=False, n (bf16) is None unless want_norm or ``norm`` is given.
-    amax_word (uint32 word on the device) takes the maximum |n| of the bf16 n."""
-    _want(x, "x", torch.bfloat16, torch.float32)
-    rows, cols = x.shape
-    dev = x.device
-    _want_vector(w, "w", cols, dev)
-    r_ptr, r_dtype, r_ld, h_ptr, h_ld = None, 0, 0, None, 0
+    amax_word (32-bit word on the device) takes the maximum |n| of the bf16 n."""
+    ptr, rows, cols, ld, dtype, dev = _rows(x, "x")
+    shape = x.shape
+    r_ptr = h_ptr = n_ptr = a_ptr = q = None
+    r_dtype = r_ld = h_ld = n_ld = 0
     if residual is not None:
-        _want(residual, "residual", torch.bfloat16, torch.float32, shape=x.shape, device=dev)
+        r_ptr, _, _, r_ld, r_dtype, _ = _rows(residual, "residual", _DTYPES, shape, dev)
         if h is None:
-            h = torch.empty((rows, cols), dtype=residual.dtype, device=dev)
-        else:
-            _want(h, "h", residual.dtype, shape=x.shape, device=dev)
-        r_ptr, r_dtype, r_ld = residual.data_ptr(), _DTYPES[residual.dtype], _pitch(residual)
-        h_ptr, h_ld = h.data_ptr(), _pitch(h)
+            h = torch.empty_like(residual, memory_format=torch.contiguous_format)
+        h_ptr, _, _, h_ld, h_dtype, _ = _rows(h, "h", _DTYPES, shape, dev)
+        if h_dtype != r_dtype:
+            raise ValueError("h has residual's dtype")
     elif h is not None:
         raise ValueError("h is written only with a residual")
-    q = None
     if out is not None or want_fp8:
         if out is None:
-            out = FP8Matrix.empty(rows, cols, dev)
-        else:
-            _want(out.codes, "out", torch.float8_e4m3fn, shape=x.shape, device=dev)
-        q = ctypes.byref(out.c())
+            out = _fp8_like(x, rows)
+        q = ctypes.byref(out.c(shape, dev))
     if norm is None and want_norm:
-        norm = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-    elif norm is not None:
-        _want(norm, "norm", torch.bfloat16, shape=x.shape, device=dev)
-    if amax_word is not None and (amax_word.device != dev or amax_word.element_size() != 4 or amax_word.numel() < 1):
-        raise ValueError("amax_word: a 32-bit word on x's device is expected")
-    _on(dev, stream, lib().add_rmsnorm_quantize, x.data_ptr(), _DTYPES[x.dtype], _pitch(x), r_ptr, r_dtype, r_ld,
-        w.data_ptr(), float(eps), rows, cols, h_ptr, h_ld, q, None if norm is None else norm.data_ptr(),
-        0 if norm is None else _pitch(norm), None if amax_word is None else amax_word.data_ptr())
+        norm = torch.empty_like(x, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
+    if norm is not None:
+        n_ptr, _, _, n_ld, n_dtype, _ = _rows(norm, "norm", _DTYPES, shape, dev)
+        if n_dtype != DTYPE_BF16:
+            raise ValueError("norm is bfloat16")
+    if amax_word is not None:
+        if amax_word.get_device() != dev or amax_word.element_size() != 4 or amax_word.numel() < 1:
+            raise ValueError("amax_word: a 32-bit word on x's device is expected")
+        a_ptr = amax_word.data_ptr()
+    _on(dev, stream, lib().add_rmsnorm_quantize, ptr, dtype, ld, r_ptr, r_dtype, r_ld, _vector(w, "w", cols, dev), eps,
+        rows, cols, h_ptr, h_ld, q, n_ptr, n_ld, a_ptr)
     return (x if residual is None else h), out, norm
 
 
-def _epilogue(M: int, N: int, dev, bias, act: int, residual, out, out_dtype):
+def _epilogue(M: int, N: int, like, dev: int, bias, act: int, residual, out, out_dtype):
+    shape = (M, N)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
-    else:
-        _want(out, "out", torch.bfloat16, torch.float32, shape=(M, N), device=dev)
-    if out.dtype not in _DTYPES:
-        raise ValueError(f"out_dtype {out.dtype}: bfloat16 or float32 is expected")
-    if bias is not None:
-        _want_vector(bias, "bias", N, dev)
+        out = like.new_empty(shape, dtype=out_dtype)
+    o_ptr, _, _, ldc, o_dtype, _ = _rows(out, "out", _DTYPES, shape, dev)
     r_ptr, r_dtype, r_ld = None, 0, 0
     if residual is not None:
-        _want(residual, "residual", torch.bfloat16, torch.float32, shape=(M, N), device=dev)
-        r_ptr, r_dtype, r_ld = residual.data_ptr(), _DTYPES[residual.dtype], _pitch(residual)
-    return out, _Epilogue(None if bias is None else bias.data_ptr(), act, r_ptr, r_dtype, r_ld, out.data_ptr(),
-                          _DTYPES[out.dtype], _pitch(out))
+        r_ptr, _, _, r_ld, r_dtype, _ = _rows(residual, "residual", _DTYPES, shape, dev)
+    return out, _Epilogue(None if bias is None else _vector(bias, "bias", N, dev), act, r_ptr, r_dtype, r_ld, o_ptr,
+                          o_dtype, ldc)
 
 
 def w8a8_gemm(A: FP8Matrix, B: FP8Matrix, bias=None, act: int = ACT_NONE, residual=None, out=None,
@@ -425,11 +434,9 @@ def w8a8_gemm(A: FP8Matrix, B: FP8Matrix, bias=None, act: int = ACT_NONE, residu
     """act(A @ B^T + bias) + residual for E4M3 operands with row scales: A [M, K]
     activations, B [N, K] weights, bias float32 [N], residual bf16 or fp32 [M, N].
     out (bf16 or fp32 [M, N]; a new tensor of out_dtype unless given) may be residual."""
-    a, b = A.c(), B.c()
-    dev = A.codes.device
-    if B.codes.device != dev:
-        raise ValueError(f"B is on {B.codes.device}, A on {dev}")
-    out, e = _epilogue(a.rows, b.rows, dev, bias, act, residual, out, out_dtype)
+    dev = A.codes.get_device()
+    a, b = A.c(), B.c(dev=dev)
+    out, e = _epilogue(a.rows, b.rows, A.codes, dev, bias, act, residual, out, out_dtype)
     _on(dev, stream, lib().w8a8_gemm, ctypes.byref(a), ctypes.byref(b), ctypes.byref(e))
     return out
 
@@ -437,11 +444,11 @@ def w8a8_gemm(A: FP8Matrix, B: FP8Matrix, bias=None, act: int = ACT_NONE, residu
 def w4a4_gemm_fused(A: NVFP4Matrix, B: NVFP4Matrix, bias=None, act: int = ACT_NONE, residual=None, out=None,
                     out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """act(A @ B^T + bias) + residual for NVFP4 operands; arguments as for w8a8_gemm."""
+    dev = A.codes.get_device()
     a, b = A.c(), B.c()
-    dev = A.codes.device
-    if B.codes.device != dev:
-        raise ValueError(f"B is on {B.codes.device}, A on {dev}")
-    out, e = _epilogue(A.rows, B.rows, dev, bias, act, residual, out, out_dtype)
+    if B.codes.get_device() != dev:
+        raise ValueError(f"B is on {B.codes.device}, A on cuda:{dev}")
+    out, e = _epilogue(A.rows, B.rows, A.codes, dev, bias, act, residual, out, out_dtype)
     _on(dev, stream, lib().w4a4_gemm_fused, ctypes.byref(a), ctypes.byref(b), ctypes.byref(e))
     return out
 
