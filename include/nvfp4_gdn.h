@@ -392,7 +392,7 @@ enum { GEMM_ACT_NONE = 0, GEMM_ACT_SILU = 1, GEMM_ACT_GELU = 2, GEMM_ACT_RELU = 
  *   residual: may be out itself, with the same type and pitch (the residual stream is
  *             then updated in place); any other overlap is not allowed.
  * Pointers need the alignment of their element type only; N and the pitches are free
- * (ldc, ld_residual >= N).  Host struct of device pointers. */
+ * (N <= ldc, ld_residual < 2^30).  Host struct of device pointers. */
 typedef struct {
     const float* bias;    /* float32 [N], or NULL */
     int32_t act;          /* GEMM_ACT_* */

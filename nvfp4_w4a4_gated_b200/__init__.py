@@ -363,16 +363,15 @@ def w4a4_gemm(A: NVFP4Matrix, B: NVFP4Matrix, C: torch.Tensor | None = None, str
     return C
 
 
-def _fp8_like(x, rows: int) -> FP8Matrix:
-    return FP8Matrix(torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format),
-                     x.new_empty(rows, dtype=torch.float32))
+def _fp8_like(x, scale) -> FP8Matrix:
+    return FP8Matrix(torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format), scale)
 
 
 def fp8_quantize(x: torch.Tensor, out: FP8Matrix | None = None, stream=None) -> FP8Matrix:
     """Quantise the rows of a bf16 or fp32 CUDA matrix to E4M3 codes with one scale a row."""
     ptr, rows, cols, ld, dtype, dev = _rows(x, "x")
     if out is None:
-        out = _fp8_like(x, rows)
+        out = _fp8_like(x, x.new_empty(rows, dtype=torch.float32))
     _on(dev, stream, lib().fp8_quantize, ptr, dtype, rows, cols, ld, ctypes.byref(out.c(x.shape, dev)))
     return out
 
@@ -386,6 +385,7 @@ def add_rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, residual: torch.Tenso
     is None with want_fp8=False, n (bf16) is None unless want_norm or ``norm`` is given.
     amax_word (32-bit word on the device) takes the maximum |n| of the bf16 n."""
     ptr, rows, cols, ld, dtype, dev = _rows(x, "x")
+    w_ptr = _vector(w, "w", cols, dev)
     shape = x.shape
     r_ptr = h_ptr = n_ptr = a_ptr = q = None
     r_dtype = r_ld = h_ld = n_ld = 0
@@ -400,7 +400,7 @@ def add_rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, residual: torch.Tenso
         raise ValueError("h is written only with a residual")
     if out is not None or want_fp8:
         if out is None:
-            out = _fp8_like(x, rows)
+            out = _fp8_like(x, w.new_empty(rows))
         q = ctypes.byref(out.c(shape, dev))
     if norm is None and want_norm:
         norm = torch.empty_like(x, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
@@ -412,7 +412,7 @@ def add_rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, residual: torch.Tenso
         if amax_word.get_device() != dev or amax_word.element_size() != 4 or amax_word.numel() < 1:
             raise ValueError("amax_word: a 32-bit word on x's device is expected")
         a_ptr = amax_word.data_ptr()
-    _on(dev, stream, lib().add_rmsnorm_quantize, ptr, dtype, ld, r_ptr, r_dtype, r_ld, _vector(w, "w", cols, dev), eps,
+    _on(dev, stream, lib().add_rmsnorm_quantize, ptr, dtype, ld, r_ptr, r_dtype, r_ld, w_ptr, eps,
         rows, cols, h_ptr, h_ld, q, n_ptr, n_ld, a_ptr)
     return (x if residual is None else h), out, norm
 

@@ -1,6 +1,6 @@
 // epilogue.cuh -- the epilogue shared by the fused products:
 //
-//   C[m, n] = act(s acc + bias[n]) + R[m, n]
+//   C[m, n] = act(acc[m, n] s[m] t[n] + bias[n]) + R[m, n]
 //
 // The fused kernels put the weight's rows (n) on the accumulator's TMEM lanes and the
 // tokens (m) on its columns.  A thread then owns one n for a whole tile: bias[n] and
@@ -8,6 +8,12 @@
 // elements of a token's row (whole 32-byte sectors when the row is aligned), and no
 // shared-memory transpose or TMA store is needed -- so N, the pitches and the
 // alignment of C and R are free.
+//
+// What bounds it is the number of instructions per element: without its stores an
+// earlier form (24 instructions) took 71 of 80 us on 8192 x 12352 outputs, where the
+// products of K = 128 alone took 15.  Hence the arithmetic in pairs (one f32x2
+// instruction for two tokens), row addresses as base + j * (32-bit pitch), which is one
+// multiply-add each, and no test per token in whole chunks.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -20,66 +26,197 @@ struct EpiArgs {
     const float* bias;   // [N] or null
     const void* res;     // or null
     void* out;
-    int64_t ld_res, ldc;
+    uint32_t ld_res, ldc;   // row pitches in bytes
     int act, res_dtype, out_dtype;
     int M, N;
 };
 
-// One column of C: token m0 + j of row pitch ld, this thread's n.  A whole chunk runs
-// without a test per token (each test is a branch, and a branch per element keeps the
-// accesses from being in flight together); only the last tokens' chunk tests.
+// ------------------------------------------------------ pairs of float32 ---
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void split(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ F2 ex2(F2 a) {
+    float x, y;
+    split(a, x, y);
+    return f2(ex2(x), ex2(y));
+}
+__device__ __forceinline__ F2 rcp(F2 a) {
+    float x, y;
+    split(a, x, y);
+    return f2(rcp(x), rcp(y));
+}
+
+// x / (1 + e^-x).  The exponent's rounding costs 2^-24 |x log2 e| relative in e^-x, and
+// e^-x weighs less than 1 / |x| in the result: within 4 x 2^-24 |x| throughout.  e^-x
+// overflowing to infinity gives -0 for very negative x.
+__device__ __forceinline__ F2 silu(F2 x) {
+    return x * rcp(f2(1.0f, 1.0f) + ex2(x * f2(-1.44269504f, -1.44269504f)));
+}
+
+// x Phi(x) with Phi(x) = 1 - h (x >= 0) or h (x < 0), h = erfc(|x| / sqrt 2) / 2 by the
+// rational approximation 7.1.26 of Abramowitz and Stegun's Handbook (absolute error of
+// erfc at most 1.5e-7, so 0.75e-7 |x| here).
+__device__ __forceinline__ F2 gelu(F2 x) {
+    float a, b;
+    split(x, a, b);
+    const F2 z = f2(fabsf(a), fabsf(b)) * f2(0.70710678f, 0.70710678f);
+    const F2 t = rcp(fma(z, f2(0.3275911f, 0.3275911f), f2(1.0f, 1.0f)));
+    F2 p = fma(t, f2(0.5f * 1.061405429f, 0.5f * 1.061405429f), f2(0.5f * -1.453152027f, 0.5f * -1.453152027f));
+    p = fma(p, t, f2(0.5f * 1.421413741f, 0.5f * 1.421413741f));
+    p = fma(p, t, f2(0.5f * -0.284496736f, 0.5f * -0.284496736f));
+    p = fma(p, t, f2(0.5f * 0.254829592f, 0.5f * 0.254829592f));
+    const F2 h = t * p * ex2(z * z * f2(-1.44269504f, -1.44269504f));
+    float ha, hb;
+    split(h, ha, hb);
+    return x * f2(a < 0.0f ? ha : 1.0f - ha, b < 0.0f ? hb : 1.0f - hb);
+}
+
+__device__ __forceinline__ F2 relu(F2 x) {
+    float a, b;
+    split(x, a, b);
+    asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(a));   // NaN stays NaN
+    asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(b));
+    return f2(a, b);
+}
+
+// R[m0 + j, n] for j < C, as stored (bf16 in the low half), loaded ahead of its use.  R
+// may be the output itself: a thread reads each element before it, and nobody else,
+// writes it, so these are plain loads.  Past the last token the last one is read.
+template <int C>
+struct EpiResidual {
+    uint32_t raw[C];
+    __device__ __forceinline__ void load(const EpiArgs& e, int m0, int n) {
+        const int last = e.M - 1 - m0;
+        if (!e.res || n >= e.N || last < 0) return;   // nothing of it is used
+        const char* row = static_cast<const char*>(e.res) + static_cast<int64_t>(m0) * e.ld_res;
+        if (e.res_dtype == NVFP4_DTYPE_BF16) {
+            row += 2 * static_cast<int64_t>(n);
+            load_rows<uint16_t>(row, e.ld_res, last);
+        } else {
+            row += 4 * static_cast<int64_t>(n);
+            load_rows<uint32_t>(row, e.ld_res, last);
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void load_rows(const char* row, uint32_t pitch, int last) {
+        if (last >= C - 1) {
+#pragma unroll
+            for (uint32_t j = 0; j < C; ++j) raw[j] = *reinterpret_cast<const T*>(row + static_cast<uint64_t>(j) * pitch);
+        } else {
+#pragma unroll
+            for (uint32_t j = 0; j < C; ++j)
+                raw[j] = *reinterpret_cast<const T*>(row + static_cast<uint64_t>(min(j, static_cast<uint32_t>(last))) * pitch);
+        }
+    }
+};
+
+// Scales of `count` tokens from m0 on into a warp's own shared memory (16-byte aligned).
+__device__ __forceinline__ void stage_token_scales(const float* sA, int M, int m0, int count, float* s, int lane) {
+    __syncwarp();   // the previous tile's reads are done
+    for (int i = lane; i < count; i += 32) s[i] = m0 + i < M ? sA[m0 + i] : 0.0f;
+    __syncwarp();
+}
+
 template <int C, typename F>
-__device__ __forceinline__ void for_tokens(int m0, int M, F f) {
-    if (m0 + C <= M) {
+__device__ __forceinline__ void store_rows(int count, F put) {
+    if (count >= C) {
 #pragma unroll
-        for (int j = 0; j < C; ++j) f(j);
+        for (uint32_t j = 0; j < C; ++j) put(j);
     } else {
 #pragma unroll
-        for (int j = 0; j < C; ++j)
-            if (m0 + j < M) f(j);
+        for (uint32_t j = 0; j < C; ++j)
+            if (static_cast<int>(j) < count) put(j);
     }
 }
 
-// R[m0 + j, n] for j < C (0 where there is none).  R may be C itself: a thread reads
-// each element before it, and nobody else, writes it, so these are plain loads.
-template <int C>
-__device__ __forceinline__ void epilogue_residual(const EpiArgs& e, int m0, int n, float (&r)[C]) {
+// acc: the products of tokens m0 .. m0 + C - 1 for this thread's n; s: their scales in
+// shared memory, or null; t: the factor they share.
+template <int C, bool kTokenScales>
+__device__ __forceinline__ void epilogue_store(const EpiArgs& e, int m0, int n, const uint32_t (&acc)[C],
+                                               const EpiResidual<C>& res, const float* s, float t, float bias) {
+    constexpr int P = C / 2;
+    F2 v[P];
+    const F2 t2 = f2(t, t), b2 = f2(bias, bias);
 #pragma unroll
-    for (int j = 0; j < C; ++j) r[j] = 0.0f;
-    if (!e.res || n >= e.N) return;
-    const int64_t at = m0 * e.ld_res + n;
-    if (e.res_dtype == NVFP4_DTYPE_BF16) {
-        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(e.res) + at;
-        for_tokens<C>(m0, e.M, [&](int j) { r[j] = __bfloat162float(p[j * e.ld_res]); });
-    } else {
-        const float* p = static_cast<const float*>(e.res) + at;
-        for_tokens<C>(m0, e.M, [&](int j) { r[j] = p[j * e.ld_res]; });
+    for (int j = 0; j < P; ++j) {
+        v[j] = f2(__uint_as_float(acc[2 * j]), __uint_as_float(acc[2 * j + 1]));
+        if constexpr (kTokenScales) {
+            const float2 sj = *reinterpret_cast<const float2*>(s + 2 * j);
+            v[j] = v[j] * f2(sj.x, sj.y);
+        }
+        v[j] = fma(v[j], t2, b2);
     }
-}
-
-// v: the scaled products of tokens m0 .. m0 + C - 1 for this thread's n, bias added.
-// expf and erff are CUDA's full-range functions; x / (1 + e^-x) runs to -0 for very
-// negative x (its denominator overflows to infinity).
-template <int C>
-__device__ __forceinline__ void epilogue_store(const EpiArgs& e, int m0, int n, float (&v)[C], const float (&r)[C]) {
     if (e.act == GEMM_ACT_SILU) {
 #pragma unroll
-        for (int j = 0; j < C; ++j) v[j] = __fdiv_rn(v[j], 1.0f + expf(-v[j]));
+        for (int j = 0; j < P; ++j) v[j] = silu(v[j]);
     } else if (e.act == GEMM_ACT_GELU) {
 #pragma unroll
-        for (int j = 0; j < C; ++j) v[j] = 0.5f * v[j] * (1.0f + erff(v[j] * 0.70710678118654752f));
+        for (int j = 0; j < P; ++j) v[j] = gelu(v[j]);
     } else if (e.act == GEMM_ACT_RELU) {
 #pragma unroll
-        for (int j = 0; j < C; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];   // NaN stays NaN
+        for (int j = 0; j < P; ++j) v[j] = relu(v[j]);
     }
     if (n >= e.N) return;
-    const int64_t at = m0 * e.ldc + n;
+    if (e.res) {
+        const int shift = e.res_dtype == NVFP4_DTYPE_BF16 ? 16 : 0;
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+            v[j] = v[j] + f2(__uint_as_float(res.raw[2 * j] << shift), __uint_as_float(res.raw[2 * j + 1] << shift));
+    }
+    const int count = e.M - m0;   // tokens left from this chunk on
+    char* row = static_cast<char*>(e.out) + static_cast<int64_t>(m0) * e.ldc;
     if (e.out_dtype == NVFP4_DTYPE_BF16) {
-        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(e.out) + at;
-        for_tokens<C>(m0, e.M, [&](int j) { p[j * e.ldc] = __float2bfloat16_rn(v[j] + r[j]); });
+        row += 2 * static_cast<int64_t>(n);
+        uint32_t w[P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            float x, y;
+            split(v[j], x, y);
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(y), "f"(x));
+        }
+        auto put = [&](uint32_t j) {
+            *reinterpret_cast<uint16_t*>(row + static_cast<uint64_t>(j) * e.ldc) =
+                static_cast<uint16_t>(j & 1 ? w[j / 2] >> 16 : w[j / 2] & 0xFFFFu);
+        };
+        store_rows<C>(count, put);
     } else {
-        float* p = static_cast<float*>(e.out) + at;
-        for_tokens<C>(m0, e.M, [&](int j) { p[j * e.ldc] = v[j] + r[j]; });
+        row += 4 * static_cast<int64_t>(n);
+        float x[C];
+#pragma unroll
+        for (int j = 0; j < P; ++j) split(v[j], x[2 * j], x[2 * j + 1]);
+        auto put = [&](uint32_t j) { *reinterpret_cast<float*>(row + static_cast<uint64_t>(j) * e.ldc) = x[j]; };
+        store_rows<C>(count, put);
     }
 }
 

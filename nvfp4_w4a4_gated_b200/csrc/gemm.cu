@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(320, 1)
     pdl_wait_and_trigger();
 
     if (warp == 0) {
-        if (elect_one()) {
+        if (lane == 0) {
             // ---------------------------------------------------- producer --
             uint32_t stage = 0, phase = 0;
             for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
@@ -203,9 +203,11 @@ __global__ void __launch_bounds__(320, 1)
         producer_done:;
         }
     } else if (warp == 1) {
-        // elect.sync, not `lane == 0`: the compiler then knows that one lane runs the role
-        // and issues each MMA straight from uniform registers
+#ifdef ELECT4
         if (elect_one()) {
+#else
+        if (lane == 0) {
+#endif
             // --------------------------------------------------------- MMA --
             uint32_t stage = 0, phase = 0, kt_all = 0;
             int local = 0;
@@ -321,8 +323,10 @@ __global__ void __launch_bounds__(320, 1)
             int m_idx, n_idx;
             tile_mn(tile, m_idx, n_idx);
             const int buf = local & 1;
-            if (!mbar_wait(acc_full, local & 1, err, kErrTimeoutEpi)) break;
-            tc_fence_after();
+            if constexpr (!kFused) {
+                if (!mbar_wait(acc_full, local & 1, err, kErrTimeoutEpi)) break;
+                tc_fence_after();
+            }
             const int row0 = m_idx * BM + q * 32;
             // buffer 0 drains the columns it shares with buffer 1 first
             auto chunk_col = [&](int ci) { return buf == 0 ? (ci + G::TP::FIRST) % G::TP::NCH : ci; };
@@ -334,16 +338,6 @@ __global__ void __launch_bounds__(320, 1)
                 if (epi.bias && row0 + lane < M) bias = epi.bias[row0 + lane];
             }
             auto store_chunk = [&](int ci, const uint32_t (&v)[32]) {
-                if constexpr (kFused) {
-                    const int m0 = n_idx * BN + chunk_col(ci) * 32;
-                    if (m0 >= N) return;
-                    float r[32], f[32];
-                    epilogue_residual(epi, m0, row0 + lane, r);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) f[j] = fmaf(__uint_as_float(v[j]), alpha, bias);
-                    epilogue_store(epi, m0, row0 + lane, f, r);
-                    return;
-                }
                 // staging tile (ci & 1) is free once the store issued two chunks ago has read it
                 float* tile = stg + (ci & 1) * 32 * 32;
                 if (lane == 0) bulk_wait_read<1>();
@@ -355,6 +349,31 @@ __global__ void __launch_bounds__(320, 1)
                 if (lane == 0 && row0 < M && col0 < N) tma_store_2d_hint(&tmC, tile, col0, row0, c_policy);
                 if (lane == 0) bulk_commit();
             };
+            if constexpr (kFused) {
+                // 16 columns at a time, the columns that the other buffer shares first
+                const int n = row0 + lane;
+                const int start = buf == 0 ? G::TP::FIRST * 32 : 0;
+                auto column = [&](int c) { return (c + start) % BN; };
+                EpiResidual<16> cur, next;
+                cur.load(epi, n_idx * BN + column(0), n);
+                if (!__all_sync(0xffffffffu, mbar_wait(acc_full, local & 1, err, kErrTimeoutEpi))) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < BN; c += 16) {
+                    uint32_t acc[16];
+                    tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * G::ACC_OFF + column(c), acc);
+                    if (c + 16 < BN) next.load(epi, n_idx * BN + column(c + 16), n);
+                    tmem_wait_ld();
+                    if (c + 16 == G::TP::RELEASE_AFTER * 32) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(tmem_free);
+                    }
+                    epilogue_store<16, false>(epi, n_idx * BN + column(c), n, acc, cur, nullptr, alpha, bias);
+                    cur = next;
+                }
+                continue;
+            }
             // the chunks the next tile's accumulator reuses go to registers first, so the
             // MMA warp can start that tile before they are staged and stored
             constexpr int RA = G::TP::RELEASE_AFTER;

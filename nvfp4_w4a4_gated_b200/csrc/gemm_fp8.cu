@@ -63,31 +63,27 @@ struct Fp8Args {
     EpiArgs epi;
 };
 
-// Scaled products of C accumulator columns (tokens m0 ..): acc * sA[m] * sB[n] + bias[n].
-// sa: lane l holds sA of token (m0 rounded down to a multiple of 32) + l.
-template <int C>
-__device__ __forceinline__ void scale_columns(const uint32_t (&acc)[C], float sa, int first, float sb, float bias,
-                                              float (&v)[C]) {
-#pragma unroll
-    for (int j = 0; j < C; ++j)
-        v[j] = fmaf(__uint_as_float(acc[j]) * __shfl_sync(0xffffffffu, sa, first + j), sb, bias);
-}
-
 // ------------------------------------------------------------ CTA-pair kernel --
 // Long prefills.  A cluster of two CTAs computes 256 weight rows x 256 tokens: CTA r
 // holds weight rows [128 r, 128 r + 128) of the tile and tokens [128 r, ...) of the
 // tile's tokens, 32 KB a stage for 128 x 256 x 128 products each.  The odd CTA's
 // copies signal the even CTA's barriers directly, so the issuing thread waits on one
-// barrier a stage.  Two accumulators of 256 columns fill TMEM: the eight epilogue
-// warps drain one while the next tile's products fill the other.
+// barrier a stage.  Two accumulators of 256 columns fill TMEM: the epilogue warps
+// drain one while the next tile's products fill the other.  Sixteen of them, because
+// short K is bound by the epilogue's instructions (epilogue.cuh): 8192 x 4096 x 256 with
+// SiLU took 43 us with eight and 38 with sixteen.  For long K the power limit binds: in
+// a loop, 8192 x 12352 x 5120 runs at 1.1 to 1.3 GHz and 2.4 PFLOP/s, 0.87 of the
+// sustained rate (twice the measured sustained bf16 rate).
 struct Pair {
-    static constexpr int STAGES = 7;
+        static constexpr int STAGES = 6;                     // 4 to 7 measured the same
+    static constexpr int EPI_WARPS = 16;
+    static constexpr int EPI_COLS = 1024 / EPI_WARPS;   // token columns per epilogue warp
     static constexpr int A_BYTES = 128 * kTileK;   // own weight rows
     static constexpr int B_BYTES = 128 * kTileK;   // own half of the tokens
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int SMEM = STAGES * STAGE_BYTES + 256 + 1024;
+    static constexpr int SMEM = STAGES * STAGE_BYTES + EPI_WARPS * EPI_COLS * 4 + 256 + 1024;
     static constexpr uint32_t IDESC = idesc_e4m3(256, 256);
-    static constexpr int THREADS = 320;
+    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
 };
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
@@ -95,13 +91,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                      const __grid_constant__ Fp8Args args) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024_shared(smem_raw);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + Pair::STAGES * Pair::STAGE_BYTES);   // even CTA's are used
+    float* scales = reinterpret_cast<float*>(smem + Pair::STAGES * Pair::STAGE_BYTES);
+    uint64_t* full = reinterpret_cast<uint64_t*>(scales + Pair::EPI_WARPS * Pair::EPI_COLS);   // even CTA's are used
     uint64_t* empty = full + Pair::STAGES;
     uint64_t* acc_full = empty + Pair::STAGES;   // [2]
-    uint64_t* acc_free = acc_full + 2;           // [2] even CTA's are used: 8 + 8 epilogue warps
+    uint64_t* acc_free = acc_full + 2;           // [2] even CTA's are used: both CTAs' epilogue warps
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_free + 2);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     const int num_m = (args.epi.M + 255) / 256, num_n = (args.epi.N + 255) / 256;
@@ -124,7 +121,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_free[i], 16);
+            mbar_init(&acc_free[i], 2 * Pair::EPI_WARPS);
         }
         fence_mbar_init();
     }
@@ -212,37 +209,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         }
     } else {
         // ---------------------------------------------------------- epilogue --
-        const int q = warp & 3, half = (warp - 2) >> 2;   // lane quarter, half of the columns
+        const int q = warp & 3, part = (warp - 2) >> 2;   // lane quarter, share of the columns
         const EpiArgs& e = args.epi;
+        float* s = scales + (warp - 2) * Pair::EPI_COLS;
         int local = 0;
         for (int tile = pair; tile < num_tiles; tile += npairs, ++local) {
             int m_idx, n_idx;
             tile_mn(tile, m_idx, n_idx);
             const int buf = local & 1;
             const int n = n_idx * 256 + rank * 128 + q * 32 + lane;
-            const int m_base = m_idx * 256 + half * 128;
+            const int m_base = m_idx * 256 + part * Pair::EPI_COLS;
+            // everything that does not depend on the accumulator, before the wait for it
             const float sb = n < e.N ? args.sB[n] : 0.0f;
             const float bias = e.bias && n < e.N ? e.bias[n] : 0.0f;
+            EpiResidual<16> cur, next;
+            cur.load(e, m_base, n);
+            stage_token_scales(args.sA, e.M, m_base, Pair::EPI_COLS, s, lane);
             // the warp stays together whichever of its lanes saw the budget run out
             if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_full[buf], (local >> 1) & 1, err, kErrTimeoutEpi))) break;
             tc_fence_after();
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + half * 128;
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + part * Pair::EPI_COLS;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                const int m0 = m_base + c * 32;
-                uint32_t acc[32];
-                tmem_ld_32x32b_x32(taddr + c * 32, acc);
-                const float sa = m0 + lane < e.M ? args.sA[m0 + lane] : 0.0f;
-                float r[32], v[32];
-                epilogue_residual(e, m0, n, r);
+            for (int c = 0; c < Pair::EPI_COLS; c += 16) {
+                uint32_t acc[16];
+                tmem_ld_32x32b_x16(taddr + c, acc);
+                if (c + 16 < Pair::EPI_COLS) next.load(e, m_base + c + 16, n);
                 tmem_wait_ld();
-                if (c == 3) {
+                if (c + 16 == Pair::EPI_COLS) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_free[buf]), 0));
+                    if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&acc_free[buf]), 0));
                 }
-                scale_columns(acc, sa, 0, sb, bias, v);
-                epilogue_store(e, m0, n, v, r);
+                epilogue_store<16, true>(e, m_base + c, n, acc, cur, s + c, sb, bias);
+                cur = next;
             }
         }
     }
@@ -272,9 +271,9 @@ struct Small {
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = 98304 / STAGE_BYTES;             // two CTAs an SM
     static constexpr int RING = STAGES * STAGE_BYTES;
-    static constexpr int SMEM = RING + 256 + 1024;
-    static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
     static constexpr int COLS = BN / SPLIT;                        // token columns per CTA at the end
+    static constexpr int SMEM = RING + 4 * COLS * 4 + 256 + 1024;
+    static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
     static constexpr int CHUNK = COLS < 16 ? COLS : 16;
     static constexpr int THREADS = 192;
     static constexpr uint32_t IDESC = idesc_e4m3(128, BN);
@@ -294,12 +293,13 @@ __global__ void __launch_bounds__(192)
     using G = Small<BN, SPLIT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024_shared(smem_raw);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::RING);
+    float* scales = reinterpret_cast<float*>(smem + G::RING);
+    uint64_t* full = reinterpret_cast<uint64_t*>(scales + (4 * G::COLS + 3) / 4 * 4);
     uint64_t* empty = full + G::STAGES;
     uint64_t* acc_full = empty + G::STAGES;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_full + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     const int rank = SPLIT > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int num_m = (args.epi.M + BN - 1) / BN;
     const int tile = blockIdx.x / SPLIT;
@@ -332,6 +332,10 @@ __global__ void __launch_bounds__(192)
 
     const int q = warp & 3;
     const int n = n_idx * 128 + q * 32 + lane;
+    const EpiArgs& e = args.epi;
+    float sb = 0.0f, bias = 0.0f;
+    EpiResidual<G::CHUNK> cur;
+    float* s = scales + (warp - 2) * G::COLS;
     if (warp == 0) {
         if (elect_one()) {
             for (int kt = kt0, i = 0; kt < kt1; ++kt, ++i) {
@@ -363,13 +367,19 @@ __global__ void __launch_bounds__(192)
             if (ok) mma_commit(acc_full);
         }
     } else {
+        // what does not depend on the accumulator, before the wait for it
+        if (n < e.N) {
+            sb = args.sB[n];
+            if (e.bias) bias = e.bias[n];
+        }
+        cur.load(e, m_idx * BN + rank * G::COLS, n);
+        stage_token_scales(args.sA, e.M, m_idx * BN + rank * G::COLS, G::COLS, s, lane);
         mbar_wait(acc_full, 0, err, kErrTimeoutEpi);   // expired: the error word says that C is not valid
         tc_fence_after();
     }
     __syncwarp();
 
     const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    const EpiArgs& e = args.epi;
     if constexpr (SPLIT > 1) {
         // partial accumulators, [column][lane row]: the ring is free, its last product done
         float* part = reinterpret_cast<float*>(smem);
@@ -386,25 +396,22 @@ __global__ void __launch_bounds__(192)
         cluster_sync();
     }
     if (warp >= 2) {
-        const float sb = n < e.N ? args.sB[n] : 0.0f;
-        const float bias = e.bias && n < e.N ? e.bias[n] : 0.0f;
 #pragma unroll 1
         for (int c = 0; c < G::COLS; c += G::CHUNK) {
             const int col = rank * G::COLS + c, m0 = m_idx * BN + col;
-            float r[G::CHUNK], v[G::CHUNK];
             uint32_t acc[G::CHUNK];
-            epilogue_residual(e, m0, n, r);
-            const float sa = lane < G::CHUNK && m0 + lane < e.M ? args.sA[m0 + lane] : 0.0f;
+            EpiResidual<G::CHUNK> next;
+            if (c + G::CHUNK < G::COLS) next.load(e, m0 + G::CHUNK, n);
             if constexpr (SPLIT > 1) {
                 const uint32_t at = smem_u32(smem) + (col * 128 + q * 32 + lane) * 4;
                 float sum[G::CHUNK];
 #pragma unroll
-                for (int s = 0; s < SPLIT; ++s) {
-                    const uint32_t from = mapa_shared(at, s);
+                for (int from_rank = 0; from_rank < SPLIT; ++from_rank) {
+                    const uint32_t from = mapa_shared(at, from_rank);
 #pragma unroll
                     for (int j = 0; j < G::CHUNK; ++j) {
                         const float p = ld_shared_cluster(from + j * 512);
-                        sum[j] = s ? sum[j] + p : p;
+                        sum[j] = from_rank ? sum[j] + p : p;
                     }
                 }
 #pragma unroll
@@ -413,8 +420,8 @@ __global__ void __launch_bounds__(192)
                 tmem_ld_cols<G::CHUNK>(taddr + c, acc);
                 tmem_wait_ld();
             }
-            scale_columns(acc, sa, 0, sb, bias, v);
-            epilogue_store(e, m0, n, v, r);
+            epilogue_store<G::CHUNK, true>(e, m0, n, acc, cur, s + c, sb, bias);
+            cur = next;
         }
     }
     tc_fence_before();
@@ -523,6 +530,9 @@ nvfp4_status validate_epilogue(const gemm_epilogue* e, int64_t M, int64_t N, Epi
     if (!known(e->out_dtype)) return fail(NVFP4_ERR_INVALID_ARG, "bad out_dtype");
     if (e->act < GEMM_ACT_NONE || e->act > GEMM_ACT_RELU) return fail(NVFP4_ERR_INVALID_ARG, "bad act");
     if (e->ldc < N) return fail(NVFP4_ERR_INVALID_ARG, "ldc < N");
+    constexpr int64_t kMostPitch = (int64_t(1) << 30) - 1;   // 32-bit byte pitches in the kernels
+    if (e->ldc > kMostPitch || (e->residual && e->ld_residual > kMostPitch))
+        return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "row pitch of out or residual too large");
     auto aligned = [](const void* p, int32_t t) {
         return reinterpret_cast<uintptr_t>(p) % (t == NVFP4_DTYPE_BF16 ? 2 : 4) == 0;
     };
@@ -539,8 +549,9 @@ nvfp4_status validate_epilogue(const gemm_epilogue* e, int64_t M, int64_t N, Epi
     out->bias = e->bias;
     out->res = e->residual;
     out->out = e->out;
-    out->ld_res = e->ld_residual;
-    out->ldc = e->ldc;
+    auto bytes = [](int64_t ld, int32_t t) { return static_cast<uint32_t>(ld * (t == NVFP4_DTYPE_BF16 ? 2 : 4)); };
+    out->ld_res = e->residual ? bytes(e->ld_residual, e->residual_dtype) : 0;
+    out->ldc = bytes(e->ldc, e->out_dtype);
     out->act = e->act;
     out->res_dtype = e->residual_dtype;
     out->out_dtype = e->out_dtype;
