@@ -190,7 +190,7 @@ _FP8 = {torch.float8_e4m3fn: 0}
 
 # The block operators' small calls last a few microseconds on the device, so their
 # wrappers read each tensor once and ask torch for the stream's handle alone.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _rows(t, name: str, dtypes=_DTYPES, shape=None, dev=None):
@@ -230,11 +230,11 @@ def _on(dev: int, stream, call, *args):
         if stream.device_index != dev:
             raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
         handle = stream.cuda_stream
-    if torch.cuda.current_device() != dev:
+    if _current_device() == dev:
+        status = call(*args, handle)
+    else:
         with torch.cuda.device(dev):
             status = call(*args, handle)
-    else:
-        status = call(*args, handle)
     if status:
         _check(status)
 
@@ -363,16 +363,21 @@ def w4a4_gemm(A: NVFP4Matrix, B: NVFP4Matrix, C: torch.Tensor | None = None, str
     return C
 
 
-def _fp8_like(x, scale) -> FP8Matrix:
-    return FP8Matrix(torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format), scale)
+def _new_fp8(x, scale):
+    """A new FP8Matrix shaped like x, around ``scale``, and its C form."""
+    codes = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
+    rows, cols = x.shape
+    return FP8Matrix(codes, scale), _Fp8(codes.data_ptr(), scale.data_ptr(), rows, cols, cols)
 
 
 def fp8_quantize(x: torch.Tensor, out: FP8Matrix | None = None, stream=None) -> FP8Matrix:
     """Quantise the rows of a bf16 or fp32 CUDA matrix to E4M3 codes with one scale a row."""
     ptr, rows, cols, ld, dtype, dev = _rows(x, "x")
     if out is None:
-        out = _fp8_like(x, x.new_empty(rows, dtype=torch.float32))
-    _on(dev, stream, lib().fp8_quantize, ptr, dtype, rows, cols, ld, ctypes.byref(out.c(x.shape, dev)))
+        out, q = _new_fp8(x, x.new_empty(rows, dtype=torch.float32))
+    else:
+        q = out.c(x.shape, dev)
+    _on(dev, stream, lib().fp8_quantize, ptr, dtype, rows, cols, ld, ctypes.byref(q))
     return out
 
 
@@ -393,35 +398,44 @@ def add_rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, residual: torch.Tenso
         r_ptr, _, _, r_ld, r_dtype, _ = _rows(residual, "residual", _DTYPES, shape, dev)
         if h is None:
             h = torch.empty_like(residual, memory_format=torch.contiguous_format)
-        h_ptr, _, _, h_ld, h_dtype, _ = _rows(h, "h", _DTYPES, shape, dev)
-        if h_dtype != r_dtype:
-            raise ValueError("h has residual's dtype")
+            h_ptr, h_ld = h.data_ptr(), cols
+        else:
+            h_ptr, _, _, h_ld, h_dtype, _ = _rows(h, "h", _DTYPES, shape, dev)
+            if h_dtype != r_dtype:
+                raise ValueError("h has residual's dtype")
     elif h is not None:
         raise ValueError("h is written only with a residual")
-    if out is not None or want_fp8:
-        if out is None:
-            out = _fp8_like(x, w.new_empty(rows))
+    if out is not None:
         q = ctypes.byref(out.c(shape, dev))
-    if norm is None and want_norm:
-        norm = torch.empty_like(x, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
+    elif want_fp8:
+        out, q = _new_fp8(x, w.new_empty(rows))
+        q = ctypes.byref(q)
     if norm is not None:
         n_ptr, _, _, n_ld, n_dtype, _ = _rows(norm, "norm", _DTYPES, shape, dev)
         if n_dtype != DTYPE_BF16:
             raise ValueError("norm is bfloat16")
+    elif want_norm:
+        norm = torch.empty_like(x, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
+        n_ptr, n_ld = norm.data_ptr(), cols
     if amax_word is not None:
         if amax_word.get_device() != dev or amax_word.element_size() != 4 or amax_word.numel() < 1:
             raise ValueError("amax_word: a 32-bit word on x's device is expected")
         a_ptr = amax_word.data_ptr()
-    _on(dev, stream, lib().add_rmsnorm_quantize, ptr, dtype, ld, r_ptr, r_dtype, r_ld, w_ptr, eps,
-        rows, cols, h_ptr, h_ld, q, n_ptr, n_ld, a_ptr)
+    _on(dev, stream, lib().add_rmsnorm_quantize, ptr, dtype, ld, r_ptr, r_dtype, r_ld, w_ptr, eps, rows, cols, h_ptr,
+        h_ld, q, n_ptr, n_ld, a_ptr)
     return (x if residual is None else h), out, norm
 
 
 def _epilogue(M: int, N: int, like, dev: int, bias, act: int, residual, out, out_dtype):
     shape = (M, N)
     if out is None:
+        o_dtype = _DTYPES.get(out_dtype)
+        if o_dtype is None:
+            raise ValueError(f"out_dtype {out_dtype}: bfloat16 or float32 is expected")
         out = like.new_empty(shape, dtype=out_dtype)
-    o_ptr, _, _, ldc, o_dtype, _ = _rows(out, "out", _DTYPES, shape, dev)
+        o_ptr, ldc = out.data_ptr(), N
+    else:
+        o_ptr, _, _, ldc, o_dtype, _ = _rows(out, "out", _DTYPES, shape, dev)
     r_ptr, r_dtype, r_ld = None, 0, 0
     if residual is not None:
         r_ptr, _, _, r_ld, r_dtype, _ = _rows(residual, "residual", _DTYPES, shape, dev)

@@ -89,6 +89,20 @@ nvfp4_status make_tmap_u8_sw128(CUtensorMap* map, const void* base, uint64_t row
     return make_tmap_u8_sw128_ld(map, base, rows, row_bytes, row_bytes, box_rows, box_bytes);
 }
 
+nvfp4_status make_tmap_atoms(CUtensorMap* map, const void* base, uint64_t atoms, uint32_t box_atoms) {
+    auto fn = encode_fn();
+    if (!fn) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+    cuuint64_t dims[2] = {128, atoms};
+    cuuint64_t strides[1] = {512};
+    cuuint32_t box[2] = {128, box_atoms};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled(atoms) failed: " + std::to_string(r));
+    return NVFP4_OK;
+}
+
 nvfp4_status make_tmap_f32_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld,
                                  uint32_t box_rows, uint32_t box_cols) {
     auto fn = encode_fn();

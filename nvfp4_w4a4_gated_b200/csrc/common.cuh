@@ -68,6 +68,8 @@ nvfp4_status make_tmap_u8_sw128(CUtensorMap* map, const void* base, uint64_t row
 // The same over rows of row_bytes bytes, ld bytes apart (ld % 16 == 0).
 nvfp4_status make_tmap_u8_sw128_ld(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes, uint64_t ld,
                                    uint32_t box_rows, uint32_t box_bytes);
+// TMA descriptor over consecutive 512-byte scale atoms, box_atoms a box, no swizzle.
+nvfp4_status make_tmap_atoms(CUtensorMap* map, const void* base, uint64_t atoms, uint32_t box_atoms);
 
 // 2-D tiled TMA descriptor over a row-major float32 matrix [rows x cols] with
 // row pitch ld elements, box box_rows x box_cols (box_cols * 4 <= 128), 128-byte swizzle.

@@ -35,11 +35,9 @@
 #include <cstdlib>
 #include <cstring>
 
-#include "epilogue.cuh"
+#include "common.cuh"
 
 namespace nvg {
-
-nvfp4_status validate_epilogue(const gemm_epilogue* e, int64_t M, int64_t N, EpiArgs* out);
 
 namespace {
 
@@ -96,16 +94,12 @@ __device__ __forceinline__ void stage_row(float* tile, int lane, const uint32_t 
     }
 }
 
-// kFused: A is the weight and B the tokens, so that the accumulator's lanes are the
-// weight's rows, and the epilogue of epilogue.cuh writes C from registers (tmC is not
-// used); the tiles, the ring and the scale writers are the same.
-template <int BN, bool kFused>
+template <int BN>
 __global__ void __launch_bounds__(320, 1)
     w4a4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmC, const uint8_t* __restrict__ sfA,
                      const uint8_t* __restrict__ sfB, const float* __restrict__ scaleA,
-                     const float* __restrict__ scaleB, int M, int N, int K, unsigned int* __restrict__ err,
-                     const __grid_constant__ EpiArgs epi) {
+                     const float* __restrict__ scaleB, int M, int N, int K, unsigned int* __restrict__ err) {
     using G = Cfg<BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024_shared(smem_raw);
@@ -203,11 +197,7 @@ __global__ void __launch_bounds__(320, 1)
         producer_done:;
         }
     } else if (warp == 1) {
-#ifdef ELECT4
-        if (elect_one()) {
-#else
         if (lane == 0) {
-#endif
             // --------------------------------------------------------- MMA --
             uint32_t stage = 0, phase = 0, kt_all = 0;
             int local = 0;
@@ -323,20 +313,14 @@ __global__ void __launch_bounds__(320, 1)
             int m_idx, n_idx;
             tile_mn(tile, m_idx, n_idx);
             const int buf = local & 1;
-            if constexpr (!kFused) {
-                if (!mbar_wait(acc_full, local & 1, err, kErrTimeoutEpi)) break;
-                tc_fence_after();
-            }
+            if (!mbar_wait(acc_full, local & 1, err, kErrTimeoutEpi)) break;
+            tc_fence_after();
             const int row0 = m_idx * BM + q * 32;
             // buffer 0 drains the columns it shares with buffer 1 first
             auto chunk_col = [&](int ci) { return buf == 0 ? (ci + G::TP::FIRST) % G::TP::NCH : ci; };
             auto chunk_addr = [&](int ci) {
                 return tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * G::ACC_OFF + chunk_col(ci) * 32;
             };
-            float bias = 0.0f;
-            if constexpr (kFused) {
-                if (epi.bias && row0 + lane < M) bias = epi.bias[row0 + lane];
-            }
             auto store_chunk = [&](int ci, const uint32_t (&v)[32]) {
                 // staging tile (ci & 1) is free once the store issued two chunks ago has read it
                 float* tile = stg + (ci & 1) * 32 * 32;
@@ -349,31 +333,6 @@ __global__ void __launch_bounds__(320, 1)
                 if (lane == 0 && row0 < M && col0 < N) tma_store_2d_hint(&tmC, tile, col0, row0, c_policy);
                 if (lane == 0) bulk_commit();
             };
-            if constexpr (kFused) {
-                // 16 columns at a time, the columns that the other buffer shares first
-                const int n = row0 + lane;
-                const int start = buf == 0 ? G::TP::FIRST * 32 : 0;
-                auto column = [&](int c) { return (c + start) % BN; };
-                EpiResidual<16> cur, next;
-                cur.load(epi, n_idx * BN + column(0), n);
-                if (!__all_sync(0xffffffffu, mbar_wait(acc_full, local & 1, err, kErrTimeoutEpi))) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < BN; c += 16) {
-                    uint32_t acc[16];
-                    tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * G::ACC_OFF + column(c), acc);
-                    if (c + 16 < BN) next.load(epi, n_idx * BN + column(c + 16), n);
-                    tmem_wait_ld();
-                    if (c + 16 == G::TP::RELEASE_AFTER * 32) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(tmem_free);
-                    }
-                    epilogue_store<16, false>(epi, n_idx * BN + column(c), n, acc, cur, nullptr, alpha, bias);
-                    cur = next;
-                }
-                continue;
-            }
             // the chunks the next tile's accumulator reuses go to registers first, so the
             // MMA warp can start that tile before they are staged and stored
             constexpr int RA = G::TP::RELEASE_AFTER;
@@ -721,39 +680,16 @@ nvfp4_status launch_gemm(const nvfp4_tensor& A, const nvfp4_tensor& B, float* C,
     s = make_tmap_f32_sw128(&tc, C, A.rows, B.rows, ldc, 32, 32);
     if (s != NVFP4_OK) return s;
     static PerDeviceOnce attr_once;
-    if ((s = smem_limit_once(attr_once, w4a4_gemm_kernel<BN, false>, G::SMEM, "cudaFuncSetAttribute(gemm smem)")) != NVFP4_OK)
+    if ((s = smem_limit_once(attr_once, w4a4_gemm_kernel<BN>, G::SMEM, "cudaFuncSetAttribute(gemm smem)")) != NVFP4_OK)
         return s;
     unsigned int* err = device_error_word();
     if (!err) return fail(NVFP4_ERR_CUDA, "device error word unavailable");
     const int tiles = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
     const int grid = tiles < num_sms() ? tiles : num_sms();
-    const cudaError_t e = launch_pdl(w4a4_gemm_kernel<BN, false>, dim3(grid), dim3(320), G::SMEM, st, ta, tb, tc, A.sf,
-                                     B.sf, A.global_scale, B.global_scale, M, N, K, err, EpiArgs{});
+    const cudaError_t e = launch_pdl(w4a4_gemm_kernel<BN>, dim3(grid), dim3(320), G::SMEM, st, ta, tb, tc, A.sf, B.sf,
+                                     A.global_scale, B.global_scale, M, N, K, err);
     if (e != cudaSuccess) return cuda_fail(e, "w4a4_gemm launch");
     return NVFP4_OK;
-}
-
-// W: the weight (the accumulator's lanes), X: the tokens (its columns).
-template <int BN>
-nvfp4_status launch_gemm_fused(const nvfp4_tensor& W, const nvfp4_tensor& X, const EpiArgs& epi, cudaStream_t st) {
-    using G = Cfg<BN>;
-    const int M = static_cast<int>(W.rows), N = static_cast<int>(X.rows), K = static_cast<int>(W.cols);
-    CUtensorMap tw, tx;
-    nvfp4_status s = make_tmap_u8_sw128(&tw, W.codes, W.rows, W.cols / 2, BM, K_TILE_BYTES);
-    if (s != NVFP4_OK) return s;
-    s = make_tmap_u8_sw128(&tx, X.codes, X.rows, X.cols / 2, BN, K_TILE_BYTES);
-    if (s != NVFP4_OK) return s;
-    static PerDeviceOnce attr_once;
-    if ((s = smem_limit_once(attr_once, w4a4_gemm_kernel<BN, true>, G::SMEM, "cudaFuncSetAttribute(fused gemm smem)")) !=
-        NVFP4_OK)
-        return s;
-    unsigned int* err = device_error_word();
-    if (!err) return fail(NVFP4_ERR_CUDA, "device error word unavailable");
-    const int tiles = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
-    const int grid = tiles < num_sms() ? tiles : num_sms();
-    const cudaError_t e = launch_pdl(w4a4_gemm_kernel<BN, true>, dim3(grid), dim3(320), G::SMEM, st, tw, tx, tw, W.sf,
-                                     X.sf, W.global_scale, X.global_scale, M, N, K, err, epi);
-    return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "w4a4_gemm_fused launch");
 }
 
 }  // namespace
@@ -803,21 +739,4 @@ extern "C" nvfp4_status w4a4_gemm(const nvfp4_tensor* A, const nvfp4_tensor* B, 
     if (A->rows > (int64_t(1) << 30) || B->rows > (int64_t(1) << 30))
         return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "M or N too large");
     return gemm_launch(*A, *B, C, ldc, as_stream(stream));
-}
-
-extern "C" nvfp4_status w4a4_gemm_fused(const nvfp4_tensor* A, const nvfp4_tensor* B, const gemm_epilogue* epilogue,
-                                        nvfp4_stream_t stream) {
-    using namespace nvg;
-    nvfp4_status s = validate_tensor(A, "A");
-    if (s == NVFP4_OK) s = validate_tensor(B, "B");
-    if (s != NVFP4_OK) return s;
-    if (A->cols != B->cols) return fail(NVFP4_ERR_INVALID_ARG, "A and B have different K");
-    if (A->rows > (int64_t(1) << 30) || B->rows > (int64_t(1) << 30))
-        return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "M or N too large");
-    EpiArgs epi = {};
-    if ((s = validate_epilogue(epilogue, A->rows, B->rows, &epi)) != NVFP4_OK) return s;
-    // the same choice as w4a4_gemm's, with the roles of the operands exchanged
-    const int64_t tiles256 = ((B->rows + BM - 1) / BM) * ((A->rows + 255) / 256);
-    if (A->rows <= 128 || tiles256 < num_sms()) return launch_gemm_fused<128>(*B, *A, epi, as_stream(stream));
-    return launch_gemm_fused<256>(*B, *A, epi, as_stream(stream));
 }
