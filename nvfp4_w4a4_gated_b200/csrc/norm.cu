@@ -107,165 +107,211 @@ struct RowArgs {
 struct NoResidual {};   // TR when nothing is added
 
 // TX: type of x; TR: type of r and h (NoResidual: h = x, not written); kNorm: false
-// for the plain row quantiser; V values per vector, NV vectors per thread.
-// kWarpRow: a warp per row, else a CTA per row.
-template <typename TX, typename TR, bool kNorm, int V, int NV, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 256 : 1024) row_kernel(const RowArgs a) {
+// for the plain row quantiser; V values per vector, NV vectors per thread and row.
+// R = 0: a CTA per row.  R > 0: a warp takes R rows at a time, all their loads in
+// flight together.
+template <typename TX, typename TR, bool kNorm, int V, int NV, int R>
+__global__ void __launch_bounds__(R ? 256 : 1024) row_kernel(const RowArgs a) {
     constexpr bool kAdd = !std::is_same<TR, NoResidual>::value;
+    constexpr int N = R ? R : 1;
     using RT = typename std::conditional<kAdd, TR, float>::type;
     pdl_wait_and_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t = kWarpRow ? lane : threadIdx.x;
-    const int stride = kWarpRow ? 32 : blockDim.x;
-    const int64_t row = kWarpRow ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
-    if (kWarpRow && row >= a.rows) return;
+    const int t = R ? lane : threadIdx.x;
+    const int stride = R ? 32 : blockDim.x;
+    const int64_t row0 = R ? (static_cast<int64_t>(blockIdx.x) * 8 + warp) * N : blockIdx.x;
+    const int64_t left = a.rows - row0;   // rows of this group: left, at most N
+    if (R && left <= 0) return;
     const int nvec = a.cols / V;
 
-    float v[NV][V];
-    const TX* x = static_cast<const TX*>(a.x) + row * a.ld_x;
+    float v[N][NV][V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = t + i * stride;
-        if (c < nvec) {
-            load_vec<V>(x + c * V, v[i]);
-        } else {
+    for (int k = 0; k < N; ++k) {
+        const TX* x = static_cast<const TX*>(a.x) + (row0 + k) * a.ld_x;
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[i][e] = 0.0f;
+        for (int i = 0; i < NV; ++i) {
+            const int c = t + i * stride;
+            if (c < nvec && k < left) {
+                load_vec<V>(x + c * V, v[k][i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[k][i][e] = 0.0f;
+            }
         }
     }
     if constexpr (kAdd) {
-        const RT* r = static_cast<const RT*>(a.r) + row * a.ld_r;
-        float rv[NV][V];
+        float rv[N][NV][V];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = t + i * stride;
-            if (c < nvec) load_vec<V>(r + c * V, rv[i]);
+        for (int k = 0; k < N; ++k) {
+            const RT* r = static_cast<const RT*>(a.r) + (row0 + k) * a.ld_r;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = t + i * stride;
+                if (c < nvec && k < left) load_vec<V>(r + c * V, rv[k][i]);
+            }
         }
-        RT* h = static_cast<RT*>(a.h) + row * a.ld_h;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = t + i * stride;
-            if (c < nvec) {
+        for (int k = 0; k < N; ++k) {
+            RT* h = static_cast<RT*>(a.h) + (row0 + k) * a.ld_h;
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[i][e] = round_to(v[i][e] + rv[i][e], static_cast<const RT*>(nullptr));
-                store_vec<V>(h + c * V, v[i]);
+            for (int i = 0; i < NV; ++i) {
+                const int c = t + i * stride;
+                if (c < nvec && k < left) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        v[k][i][e] = round_to(v[k][i][e] + rv[k][i][e], static_cast<const RT*>(nullptr));
+                    store_vec<V>(h + c * V, v[k][i]);
+                }
             }
         }
     }
 
-    float ss = 0.0f;
-    uint32_t top = 0;   // bits of the largest magnitude
+    float ss[N];
+    uint32_t top[N];   // bits of the largest magnitude
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        ss[k] = 0.0f;
+        top[k] = 0;
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = t + i * stride;
         if constexpr (kNorm) {
+            float wv[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+            for (int e = 0; e < V; ++e) wv[e] = 0.0f;
             if (c < nvec) {
-                float wv[V];
 #pragma unroll
                 for (int e = 0; e < V; e += 4) {
                     const float4 u = __ldg(reinterpret_cast<const float4*>(a.w + c * V + e));
                     wv[e] = u.x; wv[e + 1] = u.y; wv[e + 2] = u.z; wv[e + 3] = u.w;
                 }
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[i][e] *= wv[e];
             }
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    ss[k] = fmaf(v[k][i][e], v[k][i][e], ss[k]);
+                    v[k][i][e] *= wv[e];
+                }
         }
 #pragma unroll
-        for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int e = 0; e < V; ++e) top[k] = max(top[k], __float_as_uint(v[k][i][e]) & 0x7FFFFFFFu);
     }
-    top = __reduce_max_sync(0xffffffffu, top);
+#pragma unroll
+    for (int k = 0; k < N; ++k) top[k] = __reduce_max_sync(0xffffffffu, top[k]);
     if constexpr (kNorm) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < N; ++k) ss[k] += __shfl_xor_sync(0xffffffffu, ss[k], o);
     }
-    if constexpr (!kWarpRow) {
+    if constexpr (R == 0) {
         __shared__ float s_ss[32];
         __shared__ uint32_t s_top[32];
         if (lane == 0) {
-            s_ss[warp] = ss;
-            s_top[warp] = top;
+            s_ss[warp] = ss[0];
+            s_top[warp] = top[0];
         }
         __syncthreads();
         const int nwarps = blockDim.x >> 5;
-        top = __reduce_max_sync(0xffffffffu, lane < nwarps ? s_top[lane] : 0u);
+        top[0] = __reduce_max_sync(0xffffffffu, lane < nwarps ? s_top[lane] : 0u);
         if constexpr (kNorm) {
-            ss = lane < nwarps ? s_ss[lane] : 0.0f;
+            ss[0] = lane < nwarps ? s_ss[lane] : 0.0f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            for (int o = 16; o > 0; o >>= 1) ss[0] += __shfl_xor_sync(0xffffffffu, ss[0], o);
         }
     }
-    float rstd = 1.0f;
-    if constexpr (kNorm) {
-        const float ms = ss / static_cast<float>(a.cols);
-        // a row whose mean square is not a finite fp32 number has no norm
-        rstd = ms <= 3.402823466e38f ? rsqrtf(ms + a.eps) : __uint_as_float(0x7FC00000u);
-    }
-    const float amax = kNorm ? __uint_as_float(top) * rstd : __uint_as_float(top);
-    // NaN and infinity both give a NaN scale: the row decodes to NaN, not to numbers
-    const float S = amax < kAmaxFloor ? 1.0f : amax <= 3.402823466e38f ? __fdiv_rn(amax, kE4m3Max)
-                                                                       : __uint_as_float(0x7FC00000u);
-    const float inv = __frcp_rn(S);
-    if constexpr (kNorm) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+    for (int k = 0; k < N; ++k) {
+        if (k >= left) break;
+        const int64_t row = row0 + k;
+        float rstd = 1.0f;
+        if constexpr (kNorm) {
+            const float ms = ss[k] / static_cast<float>(a.cols);
+            // a row whose mean square is not a finite fp32 number has no norm
+            rstd = ms <= 3.402823466e38f ? rsqrtf(ms + a.eps) : __uint_as_float(0x7FC00000u);
+        }
+        const float amax = kNorm ? __uint_as_float(top[k]) * rstd : __uint_as_float(top[k]);
+        // NaN and infinity both give a NaN scale: the row decodes to NaN, not to numbers
+        const float S = amax < kAmaxFloor ? 1.0f : amax <= 3.402823466e38f ? __fdiv_rn(amax, kE4m3Max)
+                                                                           : __uint_as_float(0x7FC00000u);
+        const float inv = __frcp_rn(S);
+        if constexpr (kNorm) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[i][e] *= rstd;
-        if (a.n) {
-            __nv_bfloat16* n = a.n + row * a.ld_n;
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[k][i][e] *= rstd;
+            if (a.n) {
+                __nv_bfloat16* n = a.n + row * a.ld_n;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = t + i * stride;
+                    if (c < nvec) store_vec<V>(n + c * V, v[k][i]);
+                }
+                if (a.amax && t == 0) {
+                    // rounding keeps order: the largest bf16 |n| is the rounded largest |n|
+                    const uint32_t b =
+                        __float_as_uint(round_to(amax, static_cast<const __nv_bfloat16*>(nullptr))) & 0x7FFFFFFFu;
+                    if (b > *static_cast<volatile unsigned int*>(a.amax)) atomicMax(a.amax, b);
+                }
+            }
+        }
+        if (a.codes) {
+            uint8_t* q = a.codes + row * a.ld_c;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = t + i * stride;
-                if (c < nvec) store_vec<V>(n + c * V, v[i]);
-            }
-            if (a.amax && t == 0) {
-                // rounding keeps order: the largest bf16 |n| is the rounded largest |n|
-                const uint32_t b = __float_as_uint(round_to(amax, static_cast<const __nv_bfloat16*>(nullptr))) & 0x7FFFFFFFu;
-                if (b > *static_cast<volatile unsigned int*>(a.amax)) atomicMax(a.amax, b);
-            }
-        }
-    }
-    if (a.codes) {
-        uint8_t* q = a.codes + row * a.ld_c;
+                if (c < nvec) {
+                    uint32_t w[V / 4];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = t + i * stride;
-            if (c < nvec) {
-                uint32_t w[V / 4];
-#pragma unroll
-                for (int e = 0; e < V; e += 4)
-                    w[e / 4] = e4m3x4(v[i][e] * inv, v[i][e + 1] * inv, v[i][e + 2] * inv, v[i][e + 3] * inv);
-                if constexpr (V == 8)
-                    *reinterpret_cast<uint2*>(q + c * 8) = make_uint2(w[0], w[1]);
-                else
-                    *reinterpret_cast<uint32_t*>(q + c * 4) = w[0];
+                    for (int e = 0; e < V; e += 4)
+                        w[e / 4] = e4m3x4(v[k][i][e] * inv, v[k][i][e + 1] * inv, v[k][i][e + 2] * inv,
+                                          v[k][i][e + 3] * inv);
+                    if constexpr (V == 8)
+                        *reinterpret_cast<uint2*>(q + c * 8) = make_uint2(w[0], w[1]);
+                    else
+                        *reinterpret_cast<uint32_t*>(q + c * 4) = w[0];
+                }
             }
+            if (t == 0) a.scale[row] = S;
         }
-        if (t == 0) a.scale[row] = S;
     }
 }
 
+template <typename TX, typename TR, bool kNorm, int NV, int R>
+cudaError_t warp_rows_launch(const RowArgs& a, cudaStream_t st) {
+    return launch_pdl(row_kernel<TX, TR, kNorm, 4, NV, R>, dim3(static_cast<unsigned>((a.rows + 8 * R - 1) / (8 * R))),
+                      dim3(256), 0, st, a);
+}
+
+// Up to 1024 columns a warp per row, about 16 values a lane and, for short rows, several
+// rows at once (65536 x 128 fp32: 13.8 us with one row, 11.4 with four).  Longer rows a CTA per row, 16 values a thread: with
+// 32768 x 5120 that reads and writes at the copy rate (fp32 x, bf16 residual: 233 us; 8
+// values 279, 32 values 295).  Few rows want more threads a row instead (norm of 1237 x
+// 4112: 14.0 us with 8 values, 15.2 with 16; of 4096 x 5120: 30.2 and 29.4).  Rows
+// over 8192 take 32 values, in spite of a few spilled registers: two CTAs then fit an SM,
+// one works while the other waits for its row (4096 x 16384 bf16: 121 us with 16, 112).
 template <typename TX, typename TR, bool kNorm>
 cudaError_t row_launch(const RowArgs& a, cudaStream_t st) {
+    if (a.cols <= 128) return warp_rows_launch<TX, TR, kNorm, 1, 4>(a, st);
+    if (a.cols <= 256) return warp_rows_launch<TX, TR, kNorm, 2, 2>(a, st);
+    if (a.cols <= 512) return warp_rows_launch<TX, TR, kNorm, 4, 1>(a, st);
+    if (a.cols <= kWarpRowCols) return warp_rows_launch<TX, TR, kNorm, 8, 1>(a, st);
     // 16-byte vectors of the wider type
     constexpr bool kWide = std::is_same<TX, float>::value || std::is_same<TR, float>::value;
     constexpr int V = kWide ? 4 : 8;
     constexpr int U = 8 / V;                    // vectors per 8 values
     const int nvec = a.cols / V;
-    if (a.cols <= kWarpRowCols) {
-        const dim3 grid(static_cast<unsigned>((a.rows + 7) / 8)), block(256);
-        if (nvec <= 32 * U) return launch_pdl(row_kernel<TX, TR, kNorm, V, U, true>, grid, block, 0, st, a);
-        if (nvec <= 64 * U) return launch_pdl(row_kernel<TX, TR, kNorm, V, 2 * U, true>, grid, block, 0, st, a);
-        return launch_pdl(row_kernel<TX, TR, kNorm, V, 4 * U, true>, grid, block, 0, st, a);
-    }
     auto threads = [&](int nv) { return dim3(static_cast<unsigned>(((nvec + nv - 1) / nv + 31) / 32 * 32)); };
     const dim3 grid(static_cast<unsigned>(a.rows));
-    const bool few = a.rows <= num_sms();
-    if (few && nvec <= 1024 * U) return launch_pdl(row_kernel<TX, TR, kNorm, V, U, false>, grid, threads(U), 0, st, a);
-    if (nvec <= 1024 * 2 * U)
-        return launch_pdl(row_kernel<TX, TR, kNorm, V, 2 * U, false>, grid, threads(2 * U), 0, st, a);
-    return launch_pdl(row_kernel<TX, TR, kNorm, V, 4 * U, false>, grid, threads(4 * U), 0, st, a);
+    const bool few = a.rows <= static_cast<int64_t>(num_sms()) * (kNorm ? 10 : 1);
+    if (few && nvec <= 1024 * U) return launch_pdl(row_kernel<TX, TR, kNorm, V, U, 0>, grid, threads(U), 0, st, a);
+    if (nvec <= 512 * 2 * U)
+        return launch_pdl(row_kernel<TX, TR, kNorm, V, 2 * U, 0>, grid, threads(2 * U), 0, st, a);
+    return launch_pdl(row_kernel<TX, TR, kNorm, V, 4 * U, 0>, grid, threads(4 * U), 0, st, a);
 }
 
 template <typename TX>
