@@ -460,8 +460,9 @@ def w4a4_gemm_fused(A: NVFP4Matrix, B: NVFP4Matrix, bias=None, act: int = ACT_NO
     """act(A @ B^T + bias) + residual for NVFP4 operands; arguments as for w8a8_gemm."""
     dev = A.codes.get_device()
     a, b = A.c(), B.c()
-    if B.codes.get_device() != dev:
-        raise ValueError(f"B is on {B.codes.device}, A on cuda:{dev}")
+    for t in (A.sf, A.scale, B.codes, B.sf, B.scale):
+        if t.get_device() != dev:
+            raise ValueError(f"an operand is on {t.device}, A's codes on cuda:{dev}")
     out, e = _epilogue(A.rows, B.rows, A.codes, dev, bias, act, residual, out, out_dtype)
     _on(dev, stream, lib().w4a4_gemm_fused, ctypes.byref(a), ctypes.byref(b), ctypes.byref(e))
     return out

@@ -22,8 +22,9 @@
 // Behind `lane == 0` the issue itself was the limit: without copies and epilogue the
 // 8-bit pair kernel's loop ran at 2.69 PFLOP/s (8192 x 8192 x 4096), elected at 4.06.
 //
-// Every wait is bounded: on expiry the kernel records a code in the device error word
-// and returns.
+// Every wait is bounded: on expiry the kernel records a code in the device error word,
+// waits (again bounded) for the copies and products it has in flight, frees its TMEM and
+// returns; what it has not stored by then it does not store.
 #include "epilogue.cuh"
 
 namespace nvg {
@@ -143,7 +144,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
     uint64_t* empty = full + G::STAGES;
     uint64_t* acc_full = empty + G::STAGES;   // [2] by buffer
     uint64_t* acc_free = acc_full + 2;        // even CTA's are used; 8-bit: [2] by buffer, NVFP4: one, a phase a tile
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_free + 2);
+    uint64_t* drained = acc_free + 2;         // products in flight, after an expired wait
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
@@ -170,6 +172,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_free[i], 2 * G::EPI_WARPS);
         }
+        mbar_init(drained, 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -221,6 +224,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
                     }
                 }
             }
+            // after an expired wait no CTA ends before its copies (both CTAs' count here; a stage
+            // that was never filled does not wait)
+            if (!ok && rank == 0) {
+                for (uint32_t s = 0; s < G::STAGES; ++s)
+                    mbar_wait_cluster(&full[s], s < stage ? phase : phase ^ 1u, err, kErrTimeoutTma);
+            }
         }
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
@@ -236,8 +245,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
                 // 8-bit: this buffer's last tile has been read.  NVFP4: the shared columns of the
                 // tile before have been; its readers had by then finished the tile before it.
                 if (kFp4 ? local >= 1 && !mbar_wait_cluster(acc_free, (local - 1) & 1, err, kErrTimeoutMma)
-                         : local >= 2 && !mbar_wait_cluster(&acc_free[buf], ((local >> 1) - 1) & 1, err, kErrTimeoutMma))
+                         : local >= 2 && !mbar_wait_cluster(&acc_free[buf], ((local >> 1) - 1) & 1, err, kErrTimeoutMma)) {
+                    ok = false;
                     break;
+                }
                 tc_fence_after();
                 for (int kt = 0; kt < num_kt; ++kt) {
                     if (!mbar_wait_cluster(&full[stage], phase, err, kErrTimeoutMma)) {
@@ -272,6 +283,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
                 if (!ok) break;
                 mma_commit_pair(smem_u32(&acc_full[buf]));
                 mma_commit_pair(peer_acc_full + buf * 8);
+            }
+            if (!ok) {
+                mma_commit_pair(smem_u32(drained));
+                mbar_wait_cluster(drained, 0, err, kErrTimeoutMma);
             }
         }
     } else {
@@ -377,7 +392,8 @@ __global__ void __launch_bounds__(192, 2)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::RING + (G::SCALES + 15) / 16 * 16);
     uint64_t* empty = full + G::STAGES;
     uint64_t* acc_full = empty + G::STAGES;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_full + 1);
+    uint64_t* drained = acc_full + 1;   // products in flight, after an expired wait
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     const int rank = SPLIT > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -394,6 +410,7 @@ __global__ void __launch_bounds__(192, 2)
             mbar_init(&empty[s], 1);
         }
         mbar_init(acc_full, 1);
+        mbar_init(drained, 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -411,7 +428,7 @@ __global__ void __launch_bounds__(192, 2)
     pdl_wait_and_trigger();
 
     const int q = warp & 3;
-    const int n = n_idx * 128 + q * 32 + lane;
+    int n = n_idx * 128 + q * 32 + lane;
     const EpiArgs& e = args.epi;
     const int m_own = m_idx * BN + rank * G::COLS;   // first token of this CTA's share
     float t = 0.0f, bias = 0.0f;
@@ -420,7 +437,8 @@ __global__ void __launch_bounds__(192, 2)
     if (warp == 0) {
         if (elect_one()) {
             const int kb_total = args.row_bytes / kStepK;   // NVFP4: scale atoms along K
-            for (int kt = kt0, i = 0; kt < kt1; ++kt, ++i) {
+            int i = 0;
+            for (int kt = kt0; kt < kt1; ++kt, ++i) {
                 const int stage = i % G::STAGES;
                 if (!mbar_wait(&empty[stage], ((i / G::STAGES) & 1) ^ 1, err, kErrTimeoutTma)) break;
                 mbar_arrive_expect_tx(&full[stage], G::STAGE_BYTES);
@@ -435,6 +453,10 @@ __global__ void __launch_bounds__(192, 2)
                     tma_load_2d(sf + G::SF_BYTES, &maps.sx, &full[stage], 0, m_idx * kb_total + kt * kAtoms);
                 }
             }
+            // after an expired wait the CTA does not end before its copies
+            if (i < kt1 - kt0)
+                for (int k = max(0, i - G::STAGES); k < i; ++k)
+                    mbar_wait(&full[k % G::STAGES], (k / G::STAGES) & 1, err, kErrTimeoutTma);
         }
     } else if (warp == 1) {
         if (elect_one()) {
@@ -463,7 +485,12 @@ __global__ void __launch_bounds__(192, 2)
                 }
                 mma_commit(&empty[stage]);
             }
-            if (ok) mma_commit(acc_full);
+            if (ok) {
+                mma_commit(acc_full);
+            } else {
+                mma_commit(drained);
+                mbar_wait(drained, 0, err, kErrTimeoutMma);
+            }
         }
     } else {
         // what does not depend on the accumulator, before the wait for it
@@ -473,7 +500,8 @@ __global__ void __launch_bounds__(192, 2)
         }
         cur.load(e, m_own, n);
         if constexpr (!kFp4) stage_token_scales(args.sA, e.M, m_own, G::COLS, s, lane);
-        mbar_wait(acc_full, 0, err, kErrTimeoutEpi);   // expired: the error word says that C is not valid
+        // expired: nothing is stored
+        if (!__all_sync(0xffffffffu, mbar_wait(acc_full, 0, err, kErrTimeoutEpi))) n = e.N;
         tc_fence_after();
     }
     __syncwarp();

@@ -404,6 +404,10 @@ extern "C" nvfp4_status add_rmsnorm_quantize(const void* x, int32_t x_dtype, int
         if ((s = check_rows(residual, residual_dtype, ld_residual, cols, "residual")) != NVFP4_OK) return s;
         if ((s = check_rows(h, residual_dtype, ld_h, cols, "h")) != NVFP4_OK) return s;
     }
+    if (h && ((h == residual && ld_h != ld_residual) || (h == x && (x_dtype != residual_dtype || ld_h != ld_x))))
+        return fail(NVFP4_ERR_INVALID_ARG, "h may be residual or x only with the same type and pitch");
+    if (norm_bf16 && (norm_bf16 == x || norm_bf16 == residual || norm_bf16 == h))
+        return fail(NVFP4_ERR_INVALID_ARG, "norm_bf16 overlaps x, residual or h");
     if (norm_bf16 && (s = check_rows(norm_bf16, NVFP4_DTYPE_BF16, ld_norm, cols, "norm_bf16")) != NVFP4_OK) return s;
     if (out) {
         if ((s = validate_fp8(out, "out")) != NVFP4_OK) return s;

@@ -31,7 +31,7 @@ def test_quantize(status, kw):
     assert nv.lib().nvfp4_last_error()
 
 
-def norm(x=FAKE, xt=FP32, ld_x=256, r=FAKE, rt=BF16, ld_r=256, w=FAKE, eps=1e-6, rows=128, cols=256, h=FAKE, ld_h=256,
+def norm(x=FAKE + 4096, xt=FP32, ld_x=256, r=FAKE, rt=BF16, ld_r=256, w=FAKE, eps=1e-6, rows=128, cols=256, h=FAKE, ld_h=256,
          out=True, n=None, ld_n=256, amax=None):
     t = fp8(rows, cols) if out is True else out
     return nv.lib().add_rmsnorm_quantize(x, xt, ld_x, r, rt, ld_r, w, eps, rows, cols, h, ld_h,
@@ -42,9 +42,10 @@ def norm(x=FAKE, xt=FP32, ld_x=256, r=FAKE, rt=BF16, ld_r=256, w=FAKE, eps=1e-6,
     (1, dict(x=None)), (1, dict(w=None)), (1, dict(xt=9)), (1, dict(rt=-1)), (1, dict(eps=0.0)), (1, dict(eps=-1.0)),
     (1, dict(eps=float("nan"))), (1, dict(eps=float("inf"))), (1, dict(rows=0)), (1, dict(cols=0)), (2, dict(cols=40)),
     (2, dict(cols=65536, ld_x=65536)), (1, dict(h=None)), (1, dict(r=None)), (1, dict(out=None)), (1, dict(amax=FAKE)),
-    (1, dict(ld_x=248)), (1, dict(ld_r=240)), (1, dict(ld_h=240)), (1, dict(n=FAKE, ld_n=240)), (3, dict(x=FAKE + 4)),
+    (1, dict(ld_x=248)), (1, dict(ld_r=240)), (1, dict(ld_h=240)), (1, dict(n=FAKE + 64, ld_n=240)), (3, dict(x=FAKE + 4)),
     (3, dict(ld_x=258)), (3, dict(r=FAKE + 2)), (3, dict(ld_r=260)), (3, dict(h=FAKE + 8)), (3, dict(w=FAKE + 4)),
-    (3, dict(n=FAKE + 2)), (3, dict(n=FAKE, ld_n=260)), (1, dict(out=fp8(128, 240))), (3, dict(out=fp8(codes=FAKE + 4))),
+    (3, dict(n=FAKE + 2)), (3, dict(n=FAKE + 64, ld_n=260)), (1, dict(n=FAKE)), (1, dict(n=FAKE + 4096)),
+    (1, dict(ld_h=264)), (1, dict(x=FAKE, xt=BF16, ld_x=264, r=FAKE + 64)), (1, dict(x=FAKE, r=FAKE + 64)), (1, dict(out=fp8(128, 240))), (3, dict(out=fp8(codes=FAKE + 4))),
 ])
 def test_norm(status, kw):
     assert norm(**kw) == status

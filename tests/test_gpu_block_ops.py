@@ -451,3 +451,80 @@ def test_block_with_nvfp4_projections(cuda_dev):
     nv.w4a4_gemm_fused(uq, W_down, residual=h, out=h)
     check_product(h, nvfp4_value(uq), nvfp4_value(W_down), 64, None, nv.ACT_NONE, before)
     done()
+
+
+# ------------------------------------------------------------------ odd arguments --
+def test_one_operand_for_both(cuda_dev):
+    q = nv.fp8_quantize(rand((300, 272), 91))
+    C = nv.w8a8_gemm(q, q, out_dtype=F32)
+    done()
+    check_product(C, value(q), value(q), 32, None, nv.ACT_NONE, None)
+
+
+def test_output_offsets_past_32_bits(cuda_dev):
+    """An output of 2.4e9 elements, written in place over its residual."""
+    M, N, K = 40000, 60000, 16
+    A, B = fp8_pair(M, N, K, 92)
+    C = torch.ones((M, N), dtype=BF16, device="cuda")
+    nv.w8a8_gemm(A, B, residual=C, out=C)
+    done()
+    rows = torch.tensor([0, 1, 255, 256, 35790, 35791, 35792, 39936, 39999], device="cuda")
+    check_product(C[rows], value(A)[rows], value(B), 32, None, nv.ACT_NONE, torch.ones_like(C[rows]))
+
+
+def test_a_row_whose_stride_says_nothing(cuda_dev):
+    """One row of any stride is a matrix with contiguous rows."""
+    K = 256
+    base = rand((8, K), 93, BF16).contiguous()
+    x = base.as_strided((1, K), (7, 1))
+    w = torch.ones(K, device="cuda")
+    _, q, n = nv.add_rmsnorm_quantize(x, w, residual=x, want_norm=True)
+    C = nv.w8a8_gemm(nv.FP8Matrix(q.codes.as_strided((1, K), (3, 1)), q.scale), nv.fp8_quantize(base))
+    done()
+    check_codes(q, norm_ref((x.float() + x.float()).to(BF16), w))
+    assert C.shape == (1, 8)
+
+
+def test_refused_tensors(cuda_dev):
+    x, w = rand((4, 64), 94), torch.ones(64, device="cuda")
+    q = nv.fp8_quantize(x)
+    wrong = [
+        lambda: nv.fp8_quantize(x.t()),
+        lambda: nv.fp8_quantize(x.half()),
+        lambda: nv.fp8_quantize(x[0]),
+        lambda: nv.fp8_quantize(x.cpu()),
+        lambda: nv.fp8_quantize(x, out=nv.FP8Matrix.empty(4, 80)),
+        lambda: nv.add_rmsnorm_quantize(x, w[:32]),
+        lambda: nv.add_rmsnorm_quantize(x, w.bfloat16()),
+        lambda: nv.add_rmsnorm_quantize(x, w, residual=x[:3]),
+        lambda: nv.add_rmsnorm_quantize(x, w, h=x),
+        lambda: nv.add_rmsnorm_quantize(x, w, residual=x, h=x.bfloat16()),
+        lambda: nv.add_rmsnorm_quantize(x, w, norm=x),
+        lambda: nv.add_rmsnorm_quantize(x, w, want_norm=True, amax_word=torch.zeros(1)),
+        lambda: nv.w8a8_gemm(q, nv.FP8Matrix(q.codes, q.scale[:3])),
+        lambda: nv.w8a8_gemm(q, nv.FP8Matrix(q.codes.view(torch.uint8), q.scale)),
+        lambda: nv.w8a8_gemm(q, q, bias=torch.ones(5, device="cuda")),
+        lambda: nv.w8a8_gemm(q, q, out=torch.empty((4, 5), device="cuda")),
+        lambda: nv.w8a8_gemm(q, q, out_dtype=torch.float16),
+        lambda: nv.w8a8_gemm(q, q, residual=torch.ones((4, 4), device="cuda").half()),
+    ]
+    for i, call in enumerate(wrong):
+        with pytest.raises(ValueError):
+            call()
+            print("accepted", i)
+    refused = [
+        lambda: nv.fp8_quantize(torch.empty((0, 64), device="cuda")),
+        lambda: nv.fp8_quantize(rand((4, 40), 95)),
+        lambda: nv.fp8_quantize(rand((4, 64 + 4), 95)[:, 2:66]),
+        lambda: nv.fp8_quantize(x[:1].expand(4, 64)),
+        lambda: nv.add_rmsnorm_quantize(x, w, eps=0.0),
+        lambda: nv.add_rmsnorm_quantize(x, w, want_fp8=False),
+        lambda: nv.add_rmsnorm_quantize(x, w, amax_word=torch.zeros(1, device="cuda")),
+        lambda: nv.w8a8_gemm(q, nv.fp8_quantize(rand((4, 80), 96))),
+        lambda: nv.w8a8_gemm(q, q, residual=torch.ones((1, 4), device="cuda").expand(4, 4)),
+        lambda: nv.w8a8_gemm(q, q, act=9),
+    ]
+    for call in refused:
+        with pytest.raises((nv.NVFP4Error, ValueError)):
+            call()
+    done()
