@@ -360,8 +360,10 @@ struct Small {
     static constexpr int B_BYTES = BN * kTileK;
     static constexpr int SF_BYTES = kFp4 ? kAtoms * kAtomBytes : 0;   // of the weight rows, and of the tokens
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 2 * SF_BYTES;
-    // two CTAs an SM, three for 16 tokens, whose tiles bring few bytes each
-    static constexpr int STAGES = (kFp4 ? 110592 : BN == 16 ? 65536 : 98304) / STAGE_BYTES;
+    // three CTAs an SM up to 32 tokens, two above (one token x 5120 x 4096, 8-bit: 5.4 us with
+    // three, 6.0 with two, 6.8 with one)
+    static constexpr int CTAS = BN <= 32 ? 3 : 2;
+    static constexpr int STAGES = (BN <= 32 ? 73728 : 110592) / STAGE_BYTES;
     static constexpr int RING = STAGES * STAGE_BYTES;
     static constexpr int COLS = BN / SPLIT;                           // token columns per CTA at the end
     static constexpr int CHUNK = COLS == 32 ? 8 : COLS < 16 ? COLS : 16;   // two rounds of 16 would be unrolled, and spill
@@ -383,7 +385,7 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
 }
 
 template <bool kFp4, int BN, int SPLIT>
-__global__ void __launch_bounds__(192, 2)
+__global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
     fused_small_kernel(const __grid_constant__ Maps maps, const __grid_constant__ FusedArgs args) {
     using G = Small<kFp4, BN, SPLIT>;
     extern __shared__ uint8_t smem_raw[];
@@ -647,20 +649,19 @@ nvfp4_status launch_small(const Operand& X, const Operand& W, const FusedArgs& a
 
 template <bool kFp4, int BN>
 nvfp4_status launch_split(int split, const Operand& X, const Operand& W, const FusedArgs& args, cudaStream_t st) {
-    switch (split) {
-        case 4: return launch_small<kFp4, BN, 4>(X, W, args, st);
-        case 2: return launch_small<kFp4, BN, 2>(X, W, args, st);
-        default: return launch_small<kFp4, BN, 1>(X, W, args, st);
-    }
+    if constexpr (BN < 128)
+        if (split == 4) return launch_small<kFp4, BN, 4>(X, W, args, st);
+    return split == 2 ? launch_small<kFp4, BN, 2>(X, W, args, st) : launch_small<kFp4, BN, 1>(X, W, args, st);
 }
 
 // The pair kernel from 32 tiles of 256 x 256 on, when there are more than 128 tokens
 // (8-bit, 512 x 5120 x 4096, 40 tiles: 17.7 us against 19.9 for the best split; 256 x 5120
 // x 4096, 20 tiles: 16.0 against 14.6).  Below that the split-K kernel: the narrowest
-// token tile that holds the tokens, and K split while the CTAs stay within 1.5 per SM and
-// keep four k-tiles each.  Wider tiles split in two at most, because the joining costs
-// BN x 128 floats a CTA (64 x 5120 x 4096: 8.5 us with 2, 9.3 with 4; one token: 5.8
-// with 2, 5.2 with 4).
+// token tile that holds the tokens (an NVFP4 tile has to begin a 128-row scale block, so
+// more than 128 tokens take tiles of 128), and K split while the CTAs stay within 1.5 per
+// SM and keep four k-tiles each: in four at most (8-bit, 64 x 5120 x 4096: 8.2 us, 9.4 in
+// two), in two for 128 tokens, whose joining moves 64 KB a CTA (128 x 5120 x 4096: 11.0
+// and 11.0 us; NVFP4 9.6 in four, 8.5 in two).
 template <bool kFp4>
 nvfp4_status fused_launch(const Operand& X, const Operand& W, const FusedArgs& args, cudaStream_t st) {
     const int64_t M = X.rows, N = W.rows;
@@ -668,13 +669,10 @@ nvfp4_status fused_launch(const Operand& X, const Operand& W, const FusedArgs& a
     if (M > 128 && pair_tiles >= 32) return launch_pair<kFp4>(X, W, args, st);
     const int64_t n_tiles = (N + 127) / 128, most = num_sms() * 3 / 2;
     const int64_t num_kt = (args.row_bytes + kTileK - 1) / kTileK;
-    int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-    // 65 to 128 tokens as two tiles of 64 where both fit split in two (128 x 5120 x 4096:
-    // 10.2 us against 11.7); an NVFP4 tile has to begin a 128-row scale block
-    if (!kFp4 && bn == 128 && M <= 128 && n_tiles * 4 <= most && num_kt >= 8) bn = 64;
+    const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     const int64_t tiles = n_tiles * ((M + bn - 1) / bn);
     int split = 1;
-    while (split < (bn == 16 ? 4 : 2) && tiles * split * 2 <= most && num_kt / (split * 2) >= 4) split *= 2;
+    while (split < (bn < 128 ? 4 : 2) && tiles * split * 2 <= most && num_kt / (split * 2) >= 4) split *= 2;
     if (bn == 16) return launch_split<kFp4, 16>(split, X, W, args, st);
     if (bn == 32) return launch_split<kFp4, 32>(split, X, W, args, st);
     if (bn == 64) return launch_split<kFp4, 64>(split, X, W, args, st);
