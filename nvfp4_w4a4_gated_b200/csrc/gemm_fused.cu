@@ -86,12 +86,15 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
 struct Maps {
     CUtensorMap w, x;       // codes of the weight and of the tokens
     CUtensorMap sw, sx;     // NVFP4: their scale atoms
+    CUtensorMap tail;       // pair kernel: codes of the tokens in boxes of a narrow tile
 };
 
 struct FusedArgs {
     const float* sA;   // 8-bit: [M] token scales; NVFP4: the tensor's scale
     const float* sB;   // 8-bit: [N] weight-row scales; NVFP4: the tensor's scale
     int row_bytes;     // bytes of a row's K codes
+    int tail_from;     // pair kernel: the tiles from this one on are cut into
+    int tail_shift;    //   2^tail_shift narrow ones
     unsigned int* err;
     EpiArgs epi;
 };
@@ -112,6 +115,10 @@ struct FusedArgs {
 // 8-bit 8192 x 4096 x 256 with SiLU took 43 us with eight and 38 with sixteen.  For long
 // K the power limit binds: in a loop, 8-bit 8192 x 12352 x 5120 runs at 1.1 to 1.3 GHz
 // and 2.4 PFLOP/s, 0.87 of twice the measured sustained bf16 rate.
+//
+// Tiles left over for a last round that they do not fill are cut into narrow ones of 128
+// or 64 tokens (NVFP4 128, a scale block), if all of these fit that round: it then ends
+// after half or a quarter of a tile's epilogue and a shorter loop.
 template <bool kFp4>
 struct Pair {
     static constexpr int A_BYTES = 128 * kTileK;                            // own weight rows
@@ -124,7 +131,7 @@ struct Pair {
     static constexpr int EPI_COLS = 1024 / EPI_WARPS;                       // token columns per epilogue warp
     static constexpr int SCALES = kFp4 ? 0 : EPI_WARPS * EPI_COLS * 4;      // token scales of each warp
     static constexpr int SMEM = STAGES * STAGE_BYTES + SCALES + 256 + 1024;
-    static constexpr uint32_t IDESC = kFp4 ? idesc_nvf4(256, 256) : idesc_e4m3(256, 256);
+    __host__ __device__ static constexpr uint32_t idesc(int N) { return kFp4 ? idesc_nvf4(256, N) : idesc_e4m3(256, N); }
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
     // TMEM columns: a scale slot holds, per step, 4 columns for A and 8 for B
     static constexpr int SF_STEP = 12, SF_SLOT = kAtoms * SF_STEP, SF_BASE = 512 - 2 * SF_SLOT;
@@ -151,16 +158,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
     const int rank = static_cast<int>(cluster_ctarank());
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     const int num_m = (args.epi.M + 255) / 256, num_n = (args.epi.N + 255) / 256;
-    const int num_tiles = num_m * num_n;
+    const int tail_from = args.tail_from, tail_shift = args.tail_shift;
+    const int num_units = tail_from + ((num_m * num_n - tail_from) << tail_shift);
     const int num_kt = (args.row_bytes + kTileK - 1) / kTileK;
     unsigned int* err = args.err;
     // Tiles run in bands of 8 token tiles, weight tiles slowest inside a band: the
     // tiles in flight then share about as many token rows as weight rows.
-    auto tile_mn = [&](int tile, int& m_idx, int& n_idx) {
+    struct Unit {
+        int m0, n_idx, shift;   // first token, weight tile, 256 >> shift tokens
+    };
+    auto unit_of = [&](int u) {
+        Unit r;
+        r.shift = u < tail_from ? 0 : tail_shift;
+        const int cut = u - tail_from, tile = u < tail_from ? u : tail_from + (cut >> tail_shift);
         const int band = tile / (8 * num_n), first = band * 8;
         const int width = min(8, num_m - first), in = tile - band * 8 * num_n;
-        m_idx = first + in % width;
-        n_idx = in / width;
+        r.n_idx = in / width;
+        r.m0 = (first + in % width) * 256 + (u < tail_from ? 0 : (cut & ((1 << tail_shift) - 1)) << (8 - tail_shift));
+        return r;
     };
 
     if (threadIdx.x == 0) {
@@ -195,28 +210,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
             const int kb_total = args.row_bytes / kStepK;   // NVFP4: scale atoms along K
             uint32_t stage = 0, phase = 0;
             bool ok = true;
-            for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
-                int m_idx, n_idx;
-                tile_mn(tile, m_idx, n_idx);
+            for (int u = pair; u < num_units && ok; u += npairs) {
+                const Unit w = unit_of(u);
+                const CUtensorMap* x = w.shift ? &maps.tail : &maps.x;
+                const uint32_t bytes = G::A_BYTES + (G::B_BYTES >> w.shift) + G::SFA_BYTES + (G::SFB_BYTES >> w.shift);
                 for (int kt = 0; kt < num_kt; ++kt) {
                     if (!mbar_wait_cluster(&empty[stage], phase ^ 1u, err, kErrTimeoutTma)) {
                         ok = false;
                         break;
                     }
                     // the even CTA's barrier counts both CTAs' bytes
-                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * G::STAGE_BYTES);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
                     const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
                     uint8_t* st = smem + stage * G::STAGE_BYTES;
-                    tma_load_2d_pair(st, &maps.w, bar, kt * kTileK, n_idx * 256 + rank * 128);
-                    tma_load_2d_pair(st + G::A_BYTES, &maps.x, bar, kt * kTileK, m_idx * 256 + rank * 128);
+                    tma_load_2d_pair(st, &maps.w, bar, kt * kTileK, w.n_idx * 256 + rank * 128);
+                    tma_load_2d_pair(st + G::A_BYTES, x, bar, kt * kTileK, w.m0 + (rank * 128 >> w.shift));
                     if constexpr (kFp4) {
                         // four atoms of each 128-row block; past K's end or the last block they
                         // belong to rows or steps that are not used, or are zero-filled
                         uint8_t* sf = st + G::A_BYTES + G::B_BYTES;
-                        tma_load_2d_pair(sf, &maps.sw, bar, 0, (n_idx * 2 + rank) * kb_total + kt * kAtoms);
-                        for (int b = 0; b < 2; ++b)
+                        tma_load_2d_pair(sf, &maps.sw, bar, 0, (w.n_idx * 2 + rank) * kb_total + kt * kAtoms);
+                        for (int b = 0; b < 2 >> w.shift; ++b)
                             tma_load_2d_pair(sf + G::SFA_BYTES + b * kAtoms * kAtomBytes, &maps.sx, bar, 0,
-                                             (m_idx * 2 + b) * kb_total + kt * kAtoms);
+                                             (w.m0 / 128 + b) * kb_total + kt * kAtoms);
                     }
                     if (++stage == G::STAGES) {
                         stage = 0;
@@ -239,9 +255,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
             uint32_t stage = 0, phase = 0, slot = 0;
             int local = 0;
             bool ok = true;
-            for (int tile = pair; tile < num_tiles && ok; tile += npairs, ++local) {
-                const int buf = local & 1;
+            for (int u = pair; u < num_units && ok; u += npairs, ++local) {
+                const int buf = local & 1, shift = u < tail_from ? 0 : tail_shift;
                 const uint32_t acc = tmem + buf * G::ACC_OFF;
+                const uint32_t idesc = shift == 0 ? G::idesc(256) : shift == 1 ? G::idesc(128) : G::idesc(64);
                 // 8-bit: this buffer's last tile has been read.  NVFP4: the shared columns of the
                 // tile before have been; its readers had by then finished the tile before it.
                 if (kFp4 ? local >= 1 && !mbar_wait_cluster(acc_free, (local - 1) & 1, err, kErrTimeoutMma)
@@ -266,10 +283,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
                             const uint32_t src = b + G::B_BYTES + j * kAtomBytes;
                             cp_scale_atom_pair(sfa, sdesc_scale_atom(src));
                             cp_scale_atom_pair(sfb, sdesc_scale_atom(src + G::SFA_BYTES));
-                            cp_scale_atom_pair(sfb + 4, sdesc_scale_atom(src + G::SFA_BYTES + kAtoms * kAtomBytes));
-                            mma_nvf4_pair(acc, da, db, G::IDESC, sfa, sfb, accumulate);
+                            if (shift == 0)
+                                cp_scale_atom_pair(sfb + 4, sdesc_scale_atom(src + G::SFA_BYTES + kAtoms * kAtomBytes));
+                            mma_nvf4_pair(acc, da, db, idesc, sfa, sfb, accumulate);
                         } else {
-                            mma_fp8_pair(acc, da, db, G::IDESC, accumulate);
+                            mma_fp8_pair(acc, da, db, idesc, accumulate);
                         }
                     }
                     slot ^= 1u;
@@ -296,16 +314,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
         float* s = scales + (warp - 2) * G::EPI_COLS;
         const float whole = kFp4 ? __fmul_rn(*args.sA, *args.sB) : 0.0f;
         int local = 0;
-        for (int tile = pair; tile < num_tiles; tile += npairs, ++local) {
-            int m_idx, n_idx;
-            tile_mn(tile, m_idx, n_idx);
-            const int buf = local & 1;
-            const int n = n_idx * 256 + rank * 128 + q * 32 + lane;
-            // the i-th 16 columns of this warp; NVFP4: interleaved, from the shared columns on
+        for (int u = pair; u < num_units; u += npairs, ++local) {
+            const Unit w = unit_of(u);
+            const int buf = local & 1, m_tile = w.m0;
+            const int n = w.n_idx * 256 + rank * 128 + q * 32 + lane;
+            // the i-th 16 columns of this warp; NVFP4: interleaved, whole tiles from the shared
+            // columns on
+            const int first = kFp4 && buf == 0 && w.shift == 0 ? G::ACC_OFF : 0;
             auto column = [&](int i) {
-                return kFp4 ? ((part + 4 * i) * 16 + (buf == 0 ? G::ACC_OFF : 0)) & 255 : part * G::EPI_COLS + i * 16;
+                return kFp4 ? ((part + 4 * i) * 16 + first) & 255 : part * (G::EPI_COLS >> w.shift) + i * 16;
             };
-            const int m_tile = m_idx * 256;
+            const int rounds = 4 >> w.shift;
             // everything that does not depend on the accumulator, before the wait for it
             const float t = kFp4 ? whole : n < e.N ? args.sB[n] : 0.0f;
             const float bias = e.bias && n < e.N ? e.bias[n] : 0.0f;
@@ -317,13 +336,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
             tc_fence_after();
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * G::ACC_OFF;
             // the round after which this warp has read all that the next tile may overwrite
-            const int last_shared = kFp4 ? (G::SHARED - 1 - part) / 4 : 3;
+            const int last_shared = kFp4 && w.shift == 0 ? (G::SHARED - 1 - part) / 4 : rounds - 1;
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < rounds; ++i) {
                 uint32_t acc[16];
                 const int c = column(i);
                 tmem_ld_32x32b_x16(taddr + c, acc);
-                if (i < 3) next.load(e, m_tile + column(i + 1), n);
+                if (i + 1 < rounds) next.load(e, m_tile + column(i + 1), n);
                 tmem_wait_ld();
                 if (i == last_shared) {
                     tc_fence_before();
@@ -611,9 +630,18 @@ nvfp4_status launch_pair(const Operand& X, const Operand& W, const FusedArgs& ar
     });
     if (s != NVFP4_OK) return s;
     const int64_t tiles = ((X.rows + 255) / 256) * ((W.rows + 255) / 256);
-    const int most = resident[dev].load(std::memory_order_relaxed);
-    const unsigned pairs = static_cast<unsigned>(tiles < most ? tiles : most);
-    const cudaError_t e = launch_pdl(fused_pair_kernel<kFp4>, dim3(pairs * 2), dim3(G::THREADS), G::SMEM, st, maps, args);
+    const int64_t most = resident[dev].load(std::memory_order_relaxed);
+    const int64_t left = tiles % most;
+    FusedArgs a = args;
+    a.tail_shift = !kFp4 && left * 4 <= most ? 2 : left * 2 <= most ? 1 : 0;
+    a.tail_from = static_cast<int>(tiles - left);
+    if (a.tail_shift && left) {
+        s = make_tmap_u8_sw128_ld(&maps.tail, X.codes, X.rows, X.row_bytes, X.ld, 128 >> a.tail_shift, kTileK);
+        if (s != NVFP4_OK) return s;
+    }
+    const int64_t units = a.tail_from + (left << a.tail_shift);
+    const unsigned pairs = static_cast<unsigned>(units < most ? units : most);
+    const cudaError_t e = launch_pdl(fused_pair_kernel<kFp4>, dim3(pairs * 2), dim3(G::THREADS), G::SMEM, st, maps, a);
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "fused pair launch");
 }
 
