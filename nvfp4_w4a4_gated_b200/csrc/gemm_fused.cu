@@ -140,17 +140,22 @@ struct Pair {
 };
 static_assert(Pair<true>::SMEM <= 232448 && Pair<false>::SMEM <= 232448, "shared memory of one CTA");
 
-template <bool kFp4>
+// kChains (8-bit): the second half of K's tiles goes to the second accumulator and the
+// epilogue adds the two, see fused_launch.
+template <bool kFp4, bool kChains>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS, 1)
     fused_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ FusedArgs args) {
     using G = Pair<kFp4>;
+    static_assert(!(kFp4 && kChains), "two chains are for 8-bit operands");
+    // one accumulator signal per tile instead of one per buffer
+    constexpr bool kOneSignal = kFp4 || kChains;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024_shared(smem_raw);
     float* scales = reinterpret_cast<float*>(smem + G::STAGES * G::STAGE_BYTES);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::STAGES * G::STAGE_BYTES + G::SCALES);   // even CTA's are used
     uint64_t* empty = full + G::STAGES;
     uint64_t* acc_full = empty + G::STAGES;   // [2] by buffer
-    uint64_t* acc_free = acc_full + 2;        // even CTA's are used; 8-bit: [2] by buffer, NVFP4: one, a phase a tile
+    uint64_t* acc_free = acc_full + 2;        // even CTA's are used; [2] by buffer, or one with a phase a tile (kOneSignal)
     uint64_t* drained = acc_free + 2;         // products in flight, after an expired wait
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
 
@@ -256,12 +261,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
             int local = 0;
             bool ok = true;
             for (int u = pair; u < num_units && ok; u += npairs, ++local) {
-                const int buf = local & 1, shift = u < tail_from ? 0 : tail_shift;
-                const uint32_t acc = tmem + buf * G::ACC_OFF;
+                const int buf = kChains ? 0 : local & 1, shift = u < tail_from ? 0 : tail_shift;
+                const int second = kChains ? (num_kt + 1) / 2 : 0;   // the second chain's first tile
                 const uint32_t idesc = shift == 0 ? G::idesc(256) : shift == 1 ? G::idesc(128) : G::idesc(64);
                 // 8-bit: this buffer's last tile has been read.  NVFP4: the shared columns of the
                 // tile before have been; its readers had by then finished the tile before it.
-                if (kFp4 ? local >= 1 && !mbar_wait_cluster(acc_free, (local - 1) & 1, err, kErrTimeoutMma)
+                // Two chains: all of the tile before has been read.
+                if (kOneSignal ? local >= 1 && !mbar_wait_cluster(acc_free, (local - 1) & 1, err, kErrTimeoutMma)
                          : local >= 2 && !mbar_wait_cluster(&acc_free[buf], ((local >> 1) - 1) & 1, err, kErrTimeoutMma)) {
                     ok = false;
                     break;
@@ -275,9 +281,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
                     tc_fence_after();
                     const uint32_t a = smem_u32(smem + stage * G::STAGE_BYTES), b = a + G::A_BYTES;
                     const int nk = min(4, (args.row_bytes - kt * kTileK + kStepK - 1) / kStepK);
+                    const uint32_t acc = tmem + (kChains ? (kt >= second) * 256 : buf * G::ACC_OFF);
                     for (int j = 0; j < nk; ++j) {
                         const uint64_t da = sdesc_kmajor_sw128(a + j * kStepK), db = sdesc_kmajor_sw128(b + j * kStepK);
-                        const uint32_t accumulate = (kt > 0 || j > 0) ? 1u : 0u;
+                        const uint32_t accumulate = (j > 0 || (kt > 0 && !(kChains && kt == second))) ? 1u : 0u;
                         if constexpr (kFp4) {
                             const uint32_t sfa = tmem + G::SF_BASE + slot * G::SF_SLOT + j * G::SF_STEP, sfb = sfa + 4;
                             const uint32_t src = b + G::B_BYTES + j * kAtomBytes;
@@ -316,7 +323,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
         int local = 0;
         for (int u = pair; u < num_units; u += npairs, ++local) {
             const Unit w = unit_of(u);
-            const int buf = local & 1, m_tile = w.m0;
+            const int buf = kChains ? 0 : local & 1, m_tile = w.m0;
             const int n = w.n_idx * 256 + rank * 128 + q * 32 + lane;
             // the i-th 16 columns of this warp; NVFP4: interleaved, whole tiles from the shared
             // columns on
@@ -332,7 +339,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
             cur.load(e, m_tile + column(0), n);
             if constexpr (!kFp4) stage_token_scales(args.sA, e.M, m_tile + column(0), G::EPI_COLS, s, lane);
             // the warp stays together whichever of its lanes saw the budget run out
-            if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_full[buf], (local >> 1) & 1, err, kErrTimeoutEpi))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_full[buf], (kChains ? local : local >> 1) & 1, err, kErrTimeoutEpi))) break;
             tc_fence_after();
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * G::ACC_OFF;
             // the round after which this warp has read all that the next tile may overwrite
@@ -342,12 +349,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
                 uint32_t acc[16];
                 const int c = column(i);
                 tmem_ld_32x32b_x16(taddr + c, acc);
+                if constexpr (kChains) {
+                    uint32_t second[16];
+                    tmem_ld_32x32b_x16(taddr + 256 + c, second);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        acc[j] = __float_as_uint(__uint_as_float(acc[j]) + __uint_as_float(second[j]));
+                }
                 if (i + 1 < rounds) next.load(e, m_tile + column(i + 1), n);
                 tmem_wait_ld();
                 if (i == last_shared) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&acc_free[kFp4 ? 0 : buf]), 0));
+                    if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&acc_free[kOneSignal ? 0 : buf]), 0));
                 }
                 epilogue_store<16, !kFp4>(e, m_tile + c, n, acc, cur, s + i * 16, t, bias);
                 cur = next;
@@ -597,7 +612,7 @@ nvfp4_status operand_maps(const Operand& o, int box_rows, CUtensorMap* codes, CU
     return s;
 }
 
-template <bool kFp4>
+template <bool kFp4, bool kChains>
 nvfp4_status launch_pair(const Operand& X, const Operand& W, const FusedArgs& args, cudaStream_t st) {
     using G = Pair<kFp4>;
     Maps maps = {};
@@ -609,7 +624,7 @@ nvfp4_status launch_pair(const Operand& X, const Operand& W, const FusedArgs& ar
     int dev = 0;
     cudaGetDevice(&dev);
     s = once_per_device(once, [&]() -> nvfp4_status {
-        cudaError_t e = cudaFuncSetAttribute(fused_pair_kernel<kFp4>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
+        cudaError_t e = cudaFuncSetAttribute(fused_pair_kernel<kFp4, kChains>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(fused pair smem)");
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(num_sms() / 2 * 2);
@@ -623,7 +638,7 @@ nvfp4_status launch_pair(const Operand& X, const Operand& W, const FusedArgs& ar
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, fused_pair_kernel<kFp4>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&n, fused_pair_kernel<kFp4, kChains>, &cfg);
         if (e != cudaSuccess || n < 1) return cuda_fail(e, "fused pair occupancy");
         resident[dev].store(n < num_sms() / 2 ? n : num_sms() / 2, std::memory_order_relaxed);
         return NVFP4_OK;
@@ -641,7 +656,7 @@ nvfp4_status launch_pair(const Operand& X, const Operand& W, const FusedArgs& ar
     }
     const int64_t units = a.tail_from + (left << a.tail_shift);
     const unsigned pairs = static_cast<unsigned>(units < most ? units : most);
-    const cudaError_t e = launch_pdl(fused_pair_kernel<kFp4>, dim3(pairs * 2), dim3(G::THREADS), G::SMEM, st, maps, a);
+    const cudaError_t e = launch_pdl(fused_pair_kernel<kFp4, kChains>, dim3(pairs * 2), dim3(G::THREADS), G::SMEM, st, maps, a);
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "fused pair launch");
 }
 
@@ -682,6 +697,16 @@ nvfp4_status launch_split(int split, const Operand& X, const Operand& W, const F
     return split == 2 ? launch_small<kFp4, BN, 2>(X, W, args, st) : launch_small<kFp4, BN, 1>(X, W, args, st);
 }
 
+// k-tiles from which an 8-bit product with a float32 result is summed in at least two
+// chains.  The tensor cores' float32 accumulation does not round to nearest: against
+// float64 its error grows in proportion to the number of steps (K = 5120, 160 steps:
+// 9.6e-7 of the result's norm in one chain, 4.2e-7 in two, 1.9e-7 in four), and 30 tiles
+// (K = 3840) keep it under 7.5e-7.  A bf16 result's own rounding is 1.7e-3.  In the pair
+// kernel two chains cost the overlap of a tile's epilogue with the next tile's products
+// (8192 x 12352 x 5120: 484 us against 440 in a loop; three stages and the first chain's
+// sum in shared memory instead would have kept it, but three stages alone take 543).
+constexpr int kChainTiles = 30;
+
 // The pair kernel from 32 tiles of 256 x 256 on, when there are more than 128 tokens
 // (8-bit, 512 x 5120 x 4096, 40 tiles: 17.7 us against 19.9 for the best split; 256 x 5120
 // x 4096, 20 tiles: 16.0 against 14.6).  Below that the split-K kernel: the narrowest
@@ -694,13 +719,19 @@ template <bool kFp4>
 nvfp4_status fused_launch(const Operand& X, const Operand& W, const FusedArgs& args, cudaStream_t st) {
     const int64_t M = X.rows, N = W.rows;
     const int64_t pair_tiles = ((M + 255) / 256) * ((N + 255) / 256);
-    if (M > 128 && pair_tiles >= 32) return launch_pair<kFp4>(X, W, args, st);
-    const int64_t n_tiles = (N + 127) / 128, most = num_sms() * 3 / 2;
     const int64_t num_kt = (args.row_bytes + kTileK - 1) / kTileK;
+    if (M > 128 && pair_tiles >= 32) {
+        if constexpr (!kFp4)
+            if (args.epi.out_dtype == NVFP4_DTYPE_FP32 && num_kt >= kChainTiles)
+                return launch_pair<false, true>(X, W, args, st);
+        return launch_pair<kFp4, false>(X, W, args, st);
+    }
+    const int64_t n_tiles = (N + 127) / 128, most = num_sms() * 3 / 2;
     const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     const int64_t tiles = n_tiles * ((M + bn - 1) / bn);
     int split = 1;
     while (split < (bn < 128 ? 4 : 2) && tiles * split * 2 <= most && num_kt / (split * 2) >= 4) split *= 2;
+    if (!kFp4 && args.epi.out_dtype == NVFP4_DTYPE_FP32 && num_kt >= kChainTiles && split == 1) split = 2;
     if (bn == 16) return launch_split<kFp4, 16>(split, X, W, args, st);
     if (bn == 32) return launch_split<kFp4, 32>(split, X, W, args, st);
     if (bn == 64) return launch_split<kFp4, 64>(split, X, W, args, st);

@@ -257,6 +257,19 @@ def test_w8a8(cuda_dev, M, N, K, out_dtype):
     assert torch.equal(C, again)
 
 
+@pytest.mark.parametrize("M,N,K", [(2300, 2311, 5120), (1030, 4099, 3856), (200, 7500, 4000), (64, 15000, 3840)])
+@pytest.mark.parametrize("act,res", [(nv.ACT_NONE, None), (nv.ACT_SILU, BF16)])
+def test_w8a8_long_sums(cuda_dev, M, N, K, act, res):
+    """float32 results of long sums: summed in two chains or more."""
+    A, B = fp8_pair(M, N, K, 7)
+    bias = torch.randn(N, generator=gen(8), device="cuda")
+    r = None if res is None else rand((M, N), 9, res)
+    C = nv.w8a8_gemm(A, B, bias=bias, act=act, residual=r, out_dtype=F32)
+    done()
+    # each chain has half the steps: half the bound
+    check_product(C, value(A), value(B), 64, bias, act, r)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 515, 256), (40, 1027, 1040), (200, 333, 256), (2300, 2311, 208)])
 @pytest.mark.parametrize("act", [nv.ACT_NONE, nv.ACT_SILU, nv.ACT_GELU, nv.ACT_RELU])
 @pytest.mark.parametrize("res", [None, F32, BF16])
