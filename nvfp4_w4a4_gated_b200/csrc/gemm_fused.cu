@@ -107,9 +107,12 @@ struct FusedArgs {
 // barrier a stage.
 //
 // Two accumulators of 256 columns, one drained while the other is filled.  With E4M3
-// they are all of TMEM.  With NVFP4 two slots of scale columns (alternate k-tiles) take
-// the top 96, and the accumulators share columns 160 .. 255: the epilogue reads those
-// first, into registers, and then lets the next tile begin.
+// they are all of TMEM.  With NVFP4 the scale columns of one stage take the top 48 (the
+// tensor pipe runs one thread's copies and products in order, so the next stage's copies
+// come after the products that read this one's), and the accumulators share columns 208 ..
+// 255: each epilogue warp reads its part of those first, into registers, and then lets the
+// next tile begin.  (Two alternating stages of scale columns and 96 shared ones made the
+// next tile wait for a second round of reads: 4096 x 5120 x 4096 54 us, now 50.)
 //
 // Sixteen epilogue warps, because short K is bound by the epilogue's instructions:
 // 8-bit 8192 x 4096 x 256 with SiLU took 43 us with eight and 38 with sixteen.  For long
@@ -133,8 +136,8 @@ struct Pair {
     static constexpr int SMEM = STAGES * STAGE_BYTES + SCALES + 256 + 1024;
     __host__ __device__ static constexpr uint32_t idesc(int N) { return kFp4 ? idesc_nvf4(256, N) : idesc_e4m3(256, N); }
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-    // TMEM columns: a scale slot holds, per step, 4 columns for A and 8 for B
-    static constexpr int SF_STEP = 12, SF_SLOT = kAtoms * SF_STEP, SF_BASE = 512 - 2 * SF_SLOT;
+    // TMEM columns: per step of a stage 4 scale columns for A and 8 for B
+    static constexpr int SF_STEP = 12, SF_BASE = 512 - kAtoms * SF_STEP;
     static constexpr int ACC_OFF = kFp4 ? SF_BASE - 256 : 256;
     static constexpr int SHARED = (256 - ACC_OFF) / 16;                     // 16-column chunks in both accumulators
 };
@@ -257,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
             // -------------------------------------------------- MMA (even CTA) --
             const uint32_t peer_acc_full = mapa_shared(smem_u32(acc_full), 1);
             const uint32_t peer_empty = mapa_shared(smem_u32(empty), 1);
-            uint32_t stage = 0, phase = 0, slot = 0;
+            uint32_t stage = 0, phase = 0;
             int local = 0;
             bool ok = true;
             for (int u = pair; u < num_units && ok; u += npairs, ++local) {
@@ -286,7 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
                         const uint64_t da = sdesc_kmajor_sw128(a + j * kStepK), db = sdesc_kmajor_sw128(b + j * kStepK);
                         const uint32_t accumulate = (j > 0 || (kt > 0 && !(kChains && kt == second))) ? 1u : 0u;
                         if constexpr (kFp4) {
-                            const uint32_t sfa = tmem + G::SF_BASE + slot * G::SF_SLOT + j * G::SF_STEP, sfb = sfa + 4;
+                            const uint32_t sfa = tmem + G::SF_BASE + j * G::SF_STEP, sfb = sfa + 4;
                             const uint32_t src = b + G::B_BYTES + j * kAtomBytes;
                             cp_scale_atom_pair(sfa, sdesc_scale_atom(src));
                             cp_scale_atom_pair(sfb, sdesc_scale_atom(src + G::SFA_BYTES));
@@ -297,7 +300,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
                             mma_fp8_pair(acc, da, db, idesc, accumulate);
                         }
                     }
-                    slot ^= 1u;
                     mma_commit_pair(smem_u32(&empty[stage]));
                     mma_commit_pair(peer_empty + stage * 8);
                     if (++stage == G::STAGES) {
@@ -404,8 +406,8 @@ struct Small {
     static constexpr int SCALES = kFp4 ? 0 : 4 * COLS * 4;
     static constexpr int SMEM = RING + SCALES + 256 + 1024;
     static constexpr int ACC_COLS = BN < 32 ? 32 : BN;
-    static constexpr int SF_STEP = 8, SF_SLOT = kAtoms * SF_STEP;     // per step 4 columns for A, 4 for B
-    static constexpr int USED_COLS = ACC_COLS + (kFp4 ? 2 * SF_SLOT : 0);
+    static constexpr int SF_STEP = 8;                                 // scale columns of a step: 4 for A, 4 for B
+    static constexpr int USED_COLS = ACC_COLS + (kFp4 ? kAtoms * SF_STEP : 0);
     static constexpr int TMEM_COLS = USED_COLS <= 32 ? 32 : USED_COLS <= 64 ? 64 : USED_COLS <= 128 ? 128 : 256;
     static constexpr int THREADS = 192;
     static constexpr uint32_t IDESC = kFp4 ? idesc_nvf4(128, BN) : idesc_e4m3(128, BN);
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
                     const uint64_t da = sdesc_kmajor_sw128(a + j * kStepK), db = sdesc_kmajor_sw128(b + j * kStepK);
                     const uint32_t accumulate = (i > 0 || j > 0) ? 1u : 0u;
                     if constexpr (kFp4) {
-                        const uint32_t sfa = tmem + G::ACC_COLS + (i & 1) * G::SF_SLOT + j * G::SF_STEP, sfb = sfa + 4;
+                        const uint32_t sfa = tmem + G::ACC_COLS + j * G::SF_STEP, sfb = sfa + 4;
                         const uint32_t src = b + G::B_BYTES + j * kAtomBytes;
                         cp_scale_atom(sfa, sdesc_scale_atom(src));
                         cp_scale_atom(sfb, sdesc_scale_atom(src + G::SF_BYTES));

@@ -350,6 +350,23 @@ def test_w4a4_fused(cuda_dev, M, N, K, bias, act, res):
         C = nv.w4a4_gemm_fused(A, B, bias=b, act=act, residual=r, out_dtype=out_dtype)
         done()
         check_product(C, nvfp4_value(A), nvfp4_value(B), 64, b, act, r)
+        assert torch.equal(C, nv.w4a4_gemm_fused(A, B, bias=b, act=act, residual=r, out_dtype=out_dtype))
+
+
+@pytest.mark.parametrize("M,N,K", [(4096, 5120, 5120), (64, 12352, 5120), (300, 3000, 8192)])
+def test_w4a4_fused_long_sums(cuda_dev, M, N, K):
+    """Scales differ from block to block and from stage to stage (rows and columns of
+    very different size): a stage's scales read too early or too late would show.  Runs
+    repeat to the bit."""
+    size = torch.exp(4 * torch.rand(K, generator=gen(48), device="cuda"))
+    A = nv.nvfp4_quantize(rand((M, K), 49) * size)
+    B = nv.nvfp4_quantize(rand((N, K), 50) / size.flip(0))
+    C = nv.w4a4_gemm_fused(A, B, out_dtype=F32)
+    done()
+    check_product(C, nvfp4_value(A), nvfp4_value(B), 64, None, nv.ACT_NONE, None)
+    for _ in range(5):
+        assert torch.equal(C, nv.w4a4_gemm_fused(A, B, out_dtype=F32))
+    done()
 
 
 @pytest.mark.parametrize("M,N,K", [(5, 130, 256), (2300, 2311, 192)])
