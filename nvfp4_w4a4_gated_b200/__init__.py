@@ -363,10 +363,19 @@ def w4a4_gemm(A: NVFP4Matrix, B: NVFP4Matrix, C: torch.Tensor | None = None, str
     return C
 
 
-def _new_fp8(x, scale):
+def _used_on(stream, *tensors):
+    """Tensors made here for a given stream: their memory is not reused before it is done."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _new_fp8(x, scale, stream):
     """A new FP8Matrix shaped like x, around ``scale``, and its C form."""
     codes = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
     rows, cols = x.shape
+    _used_on(stream, codes, scale)
     return FP8Matrix(codes, scale), _Fp8(codes.data_ptr(), scale.data_ptr(), rows, cols, cols)
 
 
@@ -374,7 +383,7 @@ def fp8_quantize(x: torch.Tensor, out: FP8Matrix | None = None, stream=None) -> 
     """Quantise the rows of a bf16 or fp32 CUDA matrix to E4M3 codes with one scale a row."""
     ptr, rows, cols, ld, dtype, dev = _rows(x, "x")
     if out is None:
-        out, q = _new_fp8(x, x.new_empty(rows, dtype=torch.float32))
+        out, q = _new_fp8(x, x.new_empty(rows, dtype=torch.float32), stream)
     else:
         q = out.c(x.shape, dev)
     _on(dev, stream, lib().fp8_quantize, ptr, dtype, rows, cols, ld, ctypes.byref(q))
@@ -399,6 +408,7 @@ def add_rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, residual: torch.Tenso
         if h is None:
             h = torch.empty_like(residual, memory_format=torch.contiguous_format)
             h_ptr, h_ld = h.data_ptr(), cols
+            _used_on(stream, h)
         else:
             h_ptr, _, _, h_ld, h_dtype, _ = _rows(h, "h", _DTYPES, shape, dev)
             if h_dtype != r_dtype:
@@ -408,7 +418,7 @@ def add_rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, residual: torch.Tenso
     if out is not None:
         q = ctypes.byref(out.c(shape, dev))
     elif want_fp8:
-        out, q = _new_fp8(x, w.new_empty(rows))
+        out, q = _new_fp8(x, w.new_empty(rows), stream)
         q = ctypes.byref(q)
     if norm is not None:
         n_ptr, _, _, n_ld, n_dtype, _ = _rows(norm, "norm", _DTYPES, shape, dev)
@@ -417,6 +427,7 @@ def add_rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, residual: torch.Tenso
     elif want_norm:
         norm = torch.empty_like(x, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
         n_ptr, n_ld = norm.data_ptr(), cols
+        _used_on(stream, norm)
     if amax_word is not None:
         if amax_word.get_device() != dev or amax_word.element_size() != 4 or amax_word.numel() < 1:
             raise ValueError("amax_word: a 32-bit word on x's device is expected")
@@ -426,7 +437,7 @@ def add_rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, residual: torch.Tenso
     return (x if residual is None else h), out, norm
 
 
-def _epilogue(M: int, N: int, like, dev: int, bias, act: int, residual, out, out_dtype):
+def _epilogue(M: int, N: int, like, dev: int, bias, act: int, residual, out, out_dtype, stream):
     shape = (M, N)
     if out is None:
         o_dtype = _DTYPES.get(out_dtype)
@@ -434,6 +445,7 @@ def _epilogue(M: int, N: int, like, dev: int, bias, act: int, residual, out, out
             raise ValueError(f"out_dtype {out_dtype}: bfloat16 or float32 is expected")
         out = like.new_empty(shape, dtype=out_dtype)
         o_ptr, ldc = out.data_ptr(), N
+        _used_on(stream, out)
     else:
         o_ptr, _, _, ldc, o_dtype, _ = _rows(out, "out", _DTYPES, shape, dev)
     r_ptr, r_dtype, r_ld = None, 0, 0
@@ -450,7 +462,7 @@ def w8a8_gemm(A: FP8Matrix, B: FP8Matrix, bias=None, act: int = ACT_NONE, residu
     out (bf16 or fp32 [M, N]; a new tensor of out_dtype unless given) may be residual."""
     dev = A.codes.get_device()
     a, b = A.c(), B.c(dev=dev)
-    out, e = _epilogue(a.rows, b.rows, A.codes, dev, bias, act, residual, out, out_dtype)
+    out, e = _epilogue(a.rows, b.rows, A.codes, dev, bias, act, residual, out, out_dtype, stream)
     _on(dev, stream, lib().w8a8_gemm, ctypes.byref(a), ctypes.byref(b), ctypes.byref(e))
     return out
 
@@ -463,7 +475,7 @@ def w4a4_gemm_fused(A: NVFP4Matrix, B: NVFP4Matrix, bias=None, act: int = ACT_NO
     for t in (A.sf, A.scale, B.codes, B.sf, B.scale):
         if t.get_device() != dev:
             raise ValueError(f"an operand is on {t.device}, A's codes on cuda:{dev}")
-    out, e = _epilogue(A.rows, B.rows, A.codes, dev, bias, act, residual, out, out_dtype)
+    out, e = _epilogue(A.rows, B.rows, A.codes, dev, bias, act, residual, out, out_dtype, stream)
     _on(dev, stream, lib().w4a4_gemm_fused, ctypes.byref(a), ctypes.byref(b), ctypes.byref(e))
     return out
 
