@@ -84,30 +84,31 @@ __device__ __forceinline__ F2 silu(F2 x) {
     return x * rcp(f2(1.0f, 1.0f) + ex2(x * f2(-1.44269504f, -1.44269504f)));
 }
 
-// x Phi(x) with Phi(x) = 1 - h (x >= 0) or h (x < 0), h = erfc(|x| / sqrt 2) / 2 by the
-// rational approximation 7.1.26 of Abramowitz and Stegun's Handbook (absolute error of
-// erfc at most 1.5e-7, so 0.75e-7 |x| here).
-__device__ __forceinline__ F2 gelu(F2 x) {
-    float a, b;
-    split(x, a, b);
-    const F2 z = f2(fabsf(a), fabsf(b)) * f2(0.70710678f, 0.70710678f);
-    const F2 t = rcp(fma(z, f2(0.3275911f, 0.3275911f), f2(1.0f, 1.0f)));
-    F2 p = fma(t, f2(0.5f * 1.061405429f, 0.5f * 1.061405429f), f2(0.5f * -1.453152027f, 0.5f * -1.453152027f));
-    p = fma(p, t, f2(0.5f * 1.421413741f, 0.5f * 1.421413741f));
-    p = fma(p, t, f2(0.5f * -0.284496736f, 0.5f * -0.284496736f));
-    p = fma(p, t, f2(0.5f * 0.254829592f, 0.5f * 0.254829592f));
-    const F2 h = t * p * ex2(z * z * f2(-1.44269504f, -1.44269504f));
-    float ha, hb;
-    split(h, ha, hb);
-    return x * f2(a < 0.0f ? ha : 1.0f - ha, b < 0.0f ? hb : 1.0f - hb);
-}
-
 __device__ __forceinline__ F2 relu(F2 x) {
     float a, b;
     split(x, a, b);
     asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(a));   // NaN stays NaN
     asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(b));
     return f2(a, b);
+}
+
+// x Phi(x) = max(x, 0) - |x| h with h = Phi(-|x|) = erfc(|x| / sqrt 2) / 2 by the rational
+// approximation 7.1.26 of Abramowitz and Stegun's Handbook (absolute error of erfc at most
+// 1.5e-7, so 0.75e-7 |x| here).  |x| is held at 20, where h has underflowed: infinities
+// come out as infinity and 0.
+__device__ __forceinline__ F2 gelu(F2 x) {
+    float a, b;
+    split(x, a, b);
+    const F2 r = relu(x);
+    const F2 c = f2(fminf(fabsf(a), 20.0f), fminf(fabsf(b), 20.0f));
+    const F2 z = c * f2(0.70710678f, 0.70710678f);
+    const F2 t = rcp(fma(z, f2(0.3275911f, 0.3275911f), f2(1.0f, 1.0f)));
+    // minus one half of the polynomial
+    F2 p = fma(t, f2(-0.5f * 1.061405429f, -0.5f * 1.061405429f), f2(0.5f * 1.453152027f, 0.5f * 1.453152027f));
+    p = fma(p, t, f2(-0.5f * 1.421413741f, -0.5f * 1.421413741f));
+    p = fma(p, t, f2(0.5f * 0.284496736f, 0.5f * 0.284496736f));
+    p = fma(p, t, f2(-0.5f * 0.254829592f, -0.5f * 0.254829592f));
+    return fma(c, t * p * ex2(z * z * f2(-1.44269504f, -1.44269504f)), r);
 }
 
 // R[m0 + j, n] for j < C, as stored (bf16 in the low half), loaded ahead of its use.  R

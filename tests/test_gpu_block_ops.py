@@ -327,6 +327,10 @@ def test_epilogue_extremes(cuda_dev):
         want = act64(v.double(), act)
         assert torch.all((C - want).abs() <= 8 * U * v.double().abs()), (act, C, want)
         assert torch.all(torch.isfinite(C))
+    inf = torch.tensor([math.inf, -math.inf], device="cuda").repeat(7)[:N]
+    C = nv.w8a8_gemm(A, B, bias=inf, act=nv.ACT_GELU, out_dtype=F32)[0]
+    done()
+    assert torch.equal(C, inf.clamp(min=0))
 
 
 def nvfp4_value(t):
