@@ -109,9 +109,10 @@ struct NoResidual {};   // TR when nothing is added
 // TX: type of x; TR: type of r and h (NoResidual: h = x, not written); kNorm: false
 // for the plain row quantiser; V values per vector, NV vectors per thread and row.
 // R = 0: a CTA per row.  R > 0: a warp takes R rows at a time, all their loads in
-// flight together.
-template <typename TX, typename TR, bool kNorm, int V, int NV, int R>
-__global__ void __launch_bounds__(R ? 256 : 1024) row_kernel(const RowArgs a) {
+// flight together.  T: most threads of a CTA; 384 and 512 keep registers for two CTAs an
+// SM, so that one works while the other waits for its row.
+template <typename TX, typename TR, bool kNorm, int V, int NV, int R, int T>
+__global__ void __launch_bounds__(T, T == 384 || T == 512 ? 2 : 0) row_kernel(const RowArgs a) {
     constexpr bool kAdd = !std::is_same<TR, NoResidual>::value;
     constexpr int N = R ? R : 1;
     using RT = typename std::conditional<kAdd, TR, float>::type;
@@ -140,27 +141,32 @@ __global__ void __launch_bounds__(R ? 256 : 1024) row_kernel(const RowArgs a) {
         }
     }
     if constexpr (kAdd) {
-        float rv[N][NV][V];
+        // 32 values a thread in 64 registers: the residual in two halves
+        constexpr int HALF = NV * V > 16 && T >= 512 ? NV / 2 : NV;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const RT* r = static_cast<const RT*>(a.r) + (row0 + k) * a.ld_r;
+        for (int i0 = 0; i0 < NV; i0 += HALF) {
+            float rv[N][HALF][V];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = t + i * stride;
-                if (c < nvec && k < left) load_vec<V>(r + c * V, rv[k][i]);
+            for (int k = 0; k < N; ++k) {
+                const RT* r = static_cast<const RT*>(a.r) + (row0 + k) * a.ld_r;
+#pragma unroll
+                for (int i = 0; i < HALF; ++i) {
+                    const int c = t + (i0 + i) * stride;
+                    if (c < nvec && k < left) load_vec<V>(r + c * V, rv[k][i]);
+                }
             }
-        }
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            RT* h = static_cast<RT*>(a.h) + (row0 + k) * a.ld_h;
+            for (int k = 0; k < N; ++k) {
+                RT* h = static_cast<RT*>(a.h) + (row0 + k) * a.ld_h;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = t + i * stride;
-                if (c < nvec && k < left) {
+                for (int i = 0; i < HALF; ++i) {
+                    const int c = t + (i0 + i) * stride;
+                    if (c < nvec && k < left) {
 #pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        v[k][i][e] = round_to(v[k][i][e] + rv[k][i][e], static_cast<const RT*>(nullptr));
-                    store_vec<V>(h + c * V, v[k][i]);
+                        for (int e = 0; e < V; ++e)
+                            v[k][i0 + i][e] = round_to(v[k][i0 + i][e] + rv[k][i][e], static_cast<const RT*>(nullptr));
+                        store_vec<V>(h + c * V, v[k][i0 + i]);
+                    }
                 }
             }
         }
@@ -283,17 +289,19 @@ __global__ void __launch_bounds__(R ? 256 : 1024) row_kernel(const RowArgs a) {
 
 template <typename TX, typename TR, bool kNorm, int NV, int R>
 cudaError_t warp_rows_launch(const RowArgs& a, cudaStream_t st) {
-    return launch_pdl(row_kernel<TX, TR, kNorm, 4, NV, R>, dim3(static_cast<unsigned>((a.rows + 8 * R - 1) / (8 * R))),
+    return launch_pdl(row_kernel<TX, TR, kNorm, 4, NV, R, 256>, dim3(static_cast<unsigned>((a.rows + 8 * R - 1) / (8 * R))),
                       dim3(256), 0, st, a);
 }
 
 // Up to 1024 columns a warp per row, about 16 values a lane and, for short rows, several
-// rows at once (65536 x 128 fp32: 13.8 us with one row, 11.4 with four).  Longer rows a CTA per row, 16 values a thread: with
-// 32768 x 5120 that reads and writes at the copy rate (fp32 x, bf16 residual: 233 us; 8
-// values 279, 32 values 295).  Few rows want more threads a row instead (norm of 1237 x
-// 4112: 14.0 us with 8 values, 15.2 with 16; of 4096 x 5120: 30.2 and 29.4).  Rows
-// over 8192 take 32 values, in spite of a few spilled registers: two CTAs then fit an SM,
-// one works while the other waits for its row (4096 x 16384 bf16: 121 us with 16, 112).
+// rows at once (65536 x 128 fp32: 13.8 us with one row, 11.4 with four).  Longer rows a
+// CTA per row, 16 values a thread: with 32768 x 5120 that reads and writes at the copy
+// rate (fp32 x, bf16 residual: 233 us; 8 values 279, 32 values 295).  Few rows want more
+// threads a row instead (norm of 1237 x 4112: 14.0 us with 8 values, 15.2 with 16; of 4096
+// x 5120: 30.2 and 29.4).  Rows over 6144 are kept to two CTAs an SM (4096 x 8192, fp32 x:
+// 60 and 54 us; rows of 5120 lose by it, 30.0 and 33.4).  Rows over 8192 take 32 values, in
+// CTAs of at most 384 or 512 threads (4096 x 12288, fp32 x, bf16 residual: 102 us in one
+// CTA of 768 threads, 91 in two of 384; 4096 x 16384 bf16: 118 and 102).
 template <typename TX, typename TR, bool kNorm>
 cudaError_t row_launch(const RowArgs& a, cudaStream_t st) {
     if (a.cols <= 128) return warp_rows_launch<TX, TR, kNorm, 1, 4>(a, st);
@@ -308,10 +316,16 @@ cudaError_t row_launch(const RowArgs& a, cudaStream_t st) {
     auto threads = [&](int nv) { return dim3(static_cast<unsigned>(((nvec + nv - 1) / nv + 31) / 32 * 32)); };
     const dim3 grid(static_cast<unsigned>(a.rows));
     const bool few = a.rows <= static_cast<int64_t>(num_sms()) * (kNorm ? 10 : 1);
-    if (few && nvec <= 1024 * U) return launch_pdl(row_kernel<TX, TR, kNorm, V, U, 0>, grid, threads(U), 0, st, a);
+    if (few && nvec <= 1024 * U) return launch_pdl(row_kernel<TX, TR, kNorm, V, U, 0, 1024>, grid, threads(U), 0, st, a);
+    if (nvec <= 384 * 2 * U)
+        return launch_pdl(row_kernel<TX, TR, kNorm, V, 2 * U, 0, 1024>, grid, threads(2 * U), 0, st, a);
     if (nvec <= 512 * 2 * U)
-        return launch_pdl(row_kernel<TX, TR, kNorm, V, 2 * U, 0>, grid, threads(2 * U), 0, st, a);
-    return launch_pdl(row_kernel<TX, TR, kNorm, V, 4 * U, 0>, grid, threads(4 * U), 0, st, a);
+        return launch_pdl(row_kernel<TX, TR, kNorm, V, 2 * U, 0, 512>, grid, threads(2 * U), 0, st, a);
+    if (nvec <= 384 * 4 * U)
+        return launch_pdl(row_kernel<TX, TR, kNorm, V, 4 * U, 0, 384>, grid, threads(4 * U), 0, st, a);
+    if (nvec <= 512 * 4 * U)
+        return launch_pdl(row_kernel<TX, TR, kNorm, V, 4 * U, 0, 512>, grid, threads(4 * U), 0, st, a);
+    return launch_pdl(row_kernel<TX, TR, kNorm, V, 4 * U, 0, 1024>, grid, threads(4 * U), 0, st, a);
 }
 
 template <typename TX>
