@@ -190,7 +190,8 @@ _FP8 = {torch.float8_e4m3fn: 0}
 
 # The block operators' small calls last a few microseconds on the device, so their
 # wrappers read each tensor once and ask torch for the stream's handle alone.
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # absent from builds without CUDA
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _rows(t, name: str, dtypes=_DTYPES, shape=None, dev=None):

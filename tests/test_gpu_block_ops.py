@@ -16,6 +16,9 @@ Bounds, with u = 2^-24 (half a float32 step, relative):
   their own evaluation is within 8 u of the argument's magnitude.
 - an output: half a step of its type (bf16 2^-8, float32 2^-24)."""
 import math
+import subprocess
+import sys
+import threading
 
 import pytest
 import torch
@@ -429,6 +432,56 @@ def test_two_graphs_replayed_at_once(cuda_dev):
         for g, x, r, run, outs, s in chains:
             for a, b in zip(outs, run()):
                 assert torch.equal(a, b)
+
+
+def test_threads_on_their_own_streams(cuda_dev):
+    """Calls that share operands, from several host threads at once."""
+    A, B = fp8_pair(300, 3000, 528, 65)
+    want = nv.w8a8_gemm(A, B)
+    done()
+    outs = [None] * 4
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                outs[i] = nv.w8a8_gemm(A, B)
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(outs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    done()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+FIRST_CALLS = """
+import torch
+import nvfp4_w4a4_gated_b200 as nv
+x, w = torch.randn(300, 512, device="cuda"), torch.ones(512, device="cuda")
+r, W = torch.randn(300, 512, device="cuda").bfloat16(), torch.randn(9000, 512, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    q = nv.fp8_quantize(W)
+    h, a, n = nv.add_rmsnorm_quantize(x, w, residual=r, want_norm=True)
+    few = nv.FP8Matrix(a.codes[:3], a.scale[:3])
+    C, c = nv.w8a8_gemm(a, q), nv.w8a8_gemm(few, q)
+    A4, B4 = nv.nvfp4_quantize(n), nv.nvfp4_quantize(W)
+    D = nv.w4a4_gemm_fused(A4, B4, act=nv.ACT_GELU)
+for _ in range(2):
+    g.replay()
+torch.cuda.synchronize()
+nv.check_device_error()
+assert torch.equal(C, nv.w8a8_gemm(a, q)) and torch.equal(c, nv.w8a8_gemm(few, q))
+assert torch.equal(D, nv.w4a4_gemm_fused(A4, B4, act=nv.ACT_GELU))
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture(cuda_dev):
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 # -------------------------------------------------------------------- the block --
