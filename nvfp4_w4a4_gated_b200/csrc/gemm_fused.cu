@@ -388,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
 // take SPLIT consecutive ranges of K (none empty: the launch keeps four k-tiles each),
 // so that weights with few row tiles still occupy every SM.  The partial accumulators
 // meet in shared memory: each CTA leaves its own there and then adds, in rank order,
-// the BN / SPLIT token columns that are its share, read from every CTA of the cluster.
+// the token columns that are its share, read from every CTA of the cluster.
 // The order is fixed: no atomics, the same bits every time.
 template <bool kFp4, int BN, int SPLIT>
 struct Small {
@@ -401,9 +401,12 @@ struct Small {
     static constexpr int CTAS = BN <= 32 ? 3 : 2;
     static constexpr int STAGES = (BN <= 32 ? 73728 : 110592) / STAGE_BYTES;
     static constexpr int RING = STAGES * STAGE_BYTES;
-    static constexpr int COLS = BN / SPLIT;                           // token columns per CTA at the end
-    static constexpr int CHUNK = COLS == 32 ? 8 : COLS < 16 ? COLS : 16;   // two rounds of 16 would be unrolled, and spill
-    static constexpr int SCALES = kFp4 ? 0 : 4 * COLS * 4;
+    // token columns are finished in chunks, a run of them by each CTA of the cluster (a run of
+    // two chunks of 16 would be unrolled, and spill)
+    static constexpr int COLS = BN / SPLIT;
+    static constexpr int CHUNK = SPLIT == 3 ? BN / 8 : COLS == 32 ? 8 : COLS < 16 ? COLS : 16;
+    static constexpr int CHUNKS = BN / CHUNK;
+    static constexpr int SCALES = kFp4 ? 0 : 4 * BN * 4;
     static constexpr int SMEM = RING + SCALES + 256 + 1024;
     static constexpr int ACC_COLS = BN < 32 ? 32 : BN;
     static constexpr int SF_STEP = 8;                                 // scale columns of a step: 4 for A, 4 for B
@@ -468,10 +471,11 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
     const int q = warp & 3;
     int n = n_idx * 128 + q * 32 + lane;
     const EpiArgs& e = args.epi;
-    const int m_own = m_idx * BN + rank * G::COLS;   // first token of this CTA's share
+    const int m_tile = m_idx * BN;
+    const int chunk0 = G::CHUNKS * rank / SPLIT, chunk1 = G::CHUNKS * (rank + 1) / SPLIT;
     float t = 0.0f, bias = 0.0f;
     EpiResidual<G::CHUNK> cur;
-    float* s = scales + (warp - 2) * G::COLS;
+    float* s = scales + (warp - 2) * BN;
     if (warp == 0) {
         if (elect_one()) {
             const int kb_total = args.row_bytes / kStepK;   // NVFP4: scale atoms along K
@@ -536,8 +540,8 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
             t = kFp4 ? __fmul_rn(*args.sA, *args.sB) : args.sB[n];
             if (e.bias) bias = e.bias[n];
         }
-        cur.load(e, m_own, n);
-        if constexpr (!kFp4) stage_token_scales(args.sA, e.M, m_own, G::COLS, s, lane);
+        cur.load(e, m_tile + chunk0 * G::CHUNK, n);
+        if constexpr (!kFp4) stage_token_scales(args.sA, e.M, m_tile, BN, s, lane);
         // expired: nothing is stored
         if (!__all_sync(0xffffffffu, mbar_wait(acc_full, 0, err, kErrTimeoutEpi))) n = e.N;
         tc_fence_after();
@@ -562,12 +566,13 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
     }
     if (warp >= 2) {
 #pragma unroll 1
-        for (int c = 0; c < G::COLS; c += G::CHUNK) {
+        for (int k = chunk0; k < chunk1; ++k) {
+            const int c = k * G::CHUNK;
             uint32_t acc[G::CHUNK];
             EpiResidual<G::CHUNK> next;
-            if (c + G::CHUNK < G::COLS) next.load(e, m_own + c + G::CHUNK, n);
+            if (k + 1 < chunk1) next.load(e, m_tile + c + G::CHUNK, n);
             if constexpr (SPLIT > 1) {
-                const uint32_t at = smem_u32(smem) + ((rank * G::COLS + c) * 128 + q * 32 + lane) * 4;
+                const uint32_t at = smem_u32(smem) + (c * 128 + q * 32 + lane) * 4;
                 float sum[G::CHUNK];
 #pragma unroll
                 for (int from_rank = 0; from_rank < SPLIT; ++from_rank) {
@@ -584,7 +589,7 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
                 tmem_ld_cols<G::CHUNK>(taddr + c, acc);
                 tmem_wait_ld();
             }
-            epilogue_store<G::CHUNK, !kFp4>(e, m_own + c, n, acc, cur, s + c, t, bias);
+            epilogue_store<G::CHUNK, !kFp4>(e, m_tile + c, n, acc, cur, s + c, t, bias);
             cur = next;
         }
     }
@@ -696,6 +701,8 @@ template <bool kFp4, int BN>
 nvfp4_status launch_split(int split, const Operand& X, const Operand& W, const FusedArgs& args, cudaStream_t st) {
     if constexpr (BN < 128)
         if (split == 4) return launch_small<kFp4, BN, 4>(X, W, args, st);
+    if constexpr (BN > 32)
+        if (split == 3) return launch_small<kFp4, BN, 3>(X, W, args, st);
     return split == 2 ? launch_small<kFp4, BN, 2>(X, W, args, st) : launch_small<kFp4, BN, 1>(X, W, args, st);
 }
 
@@ -713,10 +720,13 @@ constexpr int kChainTiles = 30;
 // (8-bit, 512 x 5120 x 4096, 40 tiles: 17.7 us against 19.9 for the best split; 256 x 5120
 // x 4096, 20 tiles: 16.0 against 14.6).  Below that the split-K kernel: the narrowest
 // token tile that holds the tokens (an NVFP4 tile has to begin a 128-row scale block, so
-// more than 128 tokens take tiles of 128), and K split while the CTAs stay within 1.5 per
-// SM and keep four k-tiles each: in four at most (8-bit, 64 x 5120 x 4096: 8.2 us, 9.4 in
-// two), in two for 128 tokens, whose joining moves 64 KB a CTA (128 x 5120 x 4096: 11.0
-// and 11.0 us; NVFP4 9.6 in four, 8.5 in two).
+// more than 128 tokens take tiles of 128).  K is split, four k-tiles at least each:
+//   up to 32 tokens, in 2 or 4 while the CTAs stay within 1.5 per SM (one token x 5120 x
+//     4096, 8-bit: 5.4 us in 4, 5.7 in 3, 6.9 in 2);
+//   above, in as many of at most 4 (3 for 128 tokens) as leave one CTA per SM, because the
+//     joining moves 32 or 64 KB a CTA (64 x 5120 x 4096: 7.3 us in 3, 8.0 in 4, 8.9 in 2;
+//     128 x 5120 x 4096: 9.1 in 3, 10.9 in 2), else in 2 within 1.5 per SM (64 x 12352 x
+//     5120: 15.5 in 2, 17.8 whole; in 3 the clusters no longer fit at once, 21).
 template <bool kFp4>
 nvfp4_status fused_launch(const Operand& X, const Operand& W, const FusedArgs& args, cudaStream_t st) {
     const int64_t M = X.rows, N = W.rows;
@@ -731,8 +741,13 @@ nvfp4_status fused_launch(const Operand& X, const Operand& W, const FusedArgs& a
     const int64_t n_tiles = (N + 127) / 128, most = num_sms() * 3 / 2;
     const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     const int64_t tiles = n_tiles * ((M + bn - 1) / bn);
-    int split = 1;
-    while (split < (bn < 128 ? 4 : 2) && tiles * split * 2 <= most && num_kt / (split * 2) >= 4) split *= 2;
+    auto fits = [&](int split, int64_t ctas) { return tiles * split <= ctas && num_kt / split >= 4; };
+    int split = fits(2, most) ? 2 : 1;
+    if (bn <= 32) {
+        if (fits(4, most)) split = 4;
+    } else if (fits(3, num_sms())) {
+        split = bn < 128 && fits(4, num_sms()) ? 4 : 3;
+    }
     if (!kFp4 && args.epi.out_dtype == NVFP4_DTYPE_FP32 && num_kt >= kChainTiles && split == 1) split = 2;
     if (bn == 16) return launch_split<kFp4, 16>(split, X, W, args, st);
     if (bn == 32) return launch_split<kFp4, 32>(split, X, W, args, st);
