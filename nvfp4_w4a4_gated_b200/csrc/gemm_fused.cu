@@ -97,7 +97,6 @@ struct FusedArgs {
     int tail_shift;    //   2^tail_shift narrow ones
     unsigned int* err;
     EpiArgs epi;
-    EpiArgs epi_add;   // kThroughOutput: no bias, the result itself as the residual
 };
 
 // ------------------------------------------------------------ CTA-pair kernel --
@@ -144,25 +143,15 @@ struct Pair {
 };
 static_assert(Pair<true>::SMEM <= 232448 && Pair<false>::SMEM <= 232448, "shared memory of one CTA");
 
-// How the sum over K is formed; two chains (8-bit only) halve the error of a float32
-// result, see fused_launch.
-enum Chains {
-    kOneChain,
-    kBothAccumulators,   // each half of K in an accumulator of its own, added by the epilogue: any
-                         // activation, but a tile's epilogue no longer overlaps the next tile
-    kThroughOutput,      // each half of K as a tile of its own: the first leaves its sum (with bias and
-                         // residual) in the float32 result, the second adds to it; no activation
-};
-
-template <bool kFp4, Chains kChains>
+// kChains (8-bit): the second half of K's tiles goes to the second accumulator and the
+// epilogue adds the two, see fused_launch.
+template <bool kFp4, bool kChains>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS, 1)
     fused_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ FusedArgs args) {
     using G = Pair<kFp4>;
-    static_assert(!kFp4 || kChains == kOneChain, "two chains are for 8-bit operands");
-    constexpr bool kBoth = kChains == kBothAccumulators;
-    constexpr int kHalves = kChains == kThroughOutput ? 2 : 1;
+    static_assert(!(kFp4 && kChains), "two chains are for 8-bit operands");
     // one accumulator signal per tile instead of one per buffer
-    constexpr bool kOneSignal = kFp4 || kBoth;
+    constexpr bool kOneSignal = kFp4 || kChains;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024_shared(smem_raw);
     float* scales = reinterpret_cast<float*>(smem + G::STAGES * G::STAGE_BYTES);
@@ -274,59 +263,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
             uint32_t stage = 0, phase = 0;
             int local = 0;
             bool ok = true;
-            const int middle = (num_kt + 1) / 2;   // two chains: the second one's first k-tile
-            for (int u = pair; u < num_units && ok; u += npairs) {
-                const int shift = u < tail_from ? 0 : tail_shift;
+            for (int u = pair; u < num_units && ok; u += npairs, ++local) {
+                const int buf = kChains ? 0 : local & 1, shift = u < tail_from ? 0 : tail_shift;
+                const int second = kChains ? (num_kt + 1) / 2 : 0;   // the second chain's first tile
                 const uint32_t idesc = shift == 0 ? G::idesc(256) : shift == 1 ? G::idesc(128) : G::idesc(64);
-                for (int half = 0; half < kHalves && ok; ++half, ++local) {
-                    const int buf = kBoth ? 0 : local & 1;
-                    // 8-bit: this buffer's last tile has been read.  NVFP4: the shared columns of the
-                    // tile before have been; its readers had by then finished the tile before it.
-                    // Both accumulators: all of the tile before has been read.
-                    if (kOneSignal ? local >= 1 && !mbar_wait_cluster(acc_free, (local - 1) & 1, err, kErrTimeoutMma)
-                                   : local >= 2 && !mbar_wait_cluster(&acc_free[buf], ((local >> 1) - 1) & 1, err,
-                                                                      kErrTimeoutMma)) {
+                // 8-bit: this buffer's last tile has been read.  NVFP4: the shared columns of the
+                // tile before have been; its readers had by then finished the tile before it.
+                // Two chains: all of the tile before has been read.
+                if (kOneSignal ? local >= 1 && !mbar_wait_cluster(acc_free, (local - 1) & 1, err, kErrTimeoutMma)
+                         : local >= 2 && !mbar_wait_cluster(&acc_free[buf], ((local >> 1) - 1) & 1, err, kErrTimeoutMma)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int kt = 0; kt < num_kt; ++kt) {
+                    if (!mbar_wait_cluster(&full[stage], phase, err, kErrTimeoutMma)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const int kt0 = half ? middle : 0, kt1 = kHalves == 2 && !half ? middle : num_kt;
-                    for (int kt = kt0; kt < kt1; ++kt) {
-                        if (!mbar_wait_cluster(&full[stage], phase, err, kErrTimeoutMma)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t a = smem_u32(smem + stage * G::STAGE_BYTES), b = a + G::A_BYTES;
-                        const int nk = min(4, (args.row_bytes - kt * kTileK + kStepK - 1) / kStepK);
-                        const uint32_t acc = tmem + (kBoth ? (kt >= middle) * 256 : buf * G::ACC_OFF);
-                        const bool first = kt == kt0 || (kBoth && kt == middle);   // of its chain
-                        for (int j = 0; j < nk; ++j) {
-                            const uint64_t da = sdesc_kmajor_sw128(a + j * kStepK), db = sdesc_kmajor_sw128(b + j * kStepK);
-                            const uint32_t accumulate = j > 0 || !first ? 1u : 0u;
-                            if constexpr (kFp4) {
-                                const uint32_t sfa = tmem + G::SF_BASE + j * G::SF_STEP, sfb = sfa + 4;
-                                const uint32_t src = b + G::B_BYTES + j * kAtomBytes;
-                                cp_scale_atom_pair(sfa, sdesc_scale_atom(src));
-                                cp_scale_atom_pair(sfb, sdesc_scale_atom(src + G::SFA_BYTES));
-                                if (shift == 0)
-                                    cp_scale_atom_pair(sfb + 4, sdesc_scale_atom(src + G::SFA_BYTES + kAtoms * kAtomBytes));
-                                mma_nvf4_pair(acc, da, db, idesc, sfa, sfb, accumulate);
-                            } else {
-                                mma_fp8_pair(acc, da, db, idesc, accumulate);
-                            }
-                        }
-                        mma_commit_pair(smem_u32(&empty[stage]));
-                        mma_commit_pair(peer_empty + stage * 8);
-                        if (++stage == G::STAGES) {
-                            stage = 0;
-                            phase ^= 1u;
+                    const uint32_t a = smem_u32(smem + stage * G::STAGE_BYTES), b = a + G::A_BYTES;
+                    const int nk = min(4, (args.row_bytes - kt * kTileK + kStepK - 1) / kStepK);
+                    const uint32_t acc = tmem + (kChains ? (kt >= second) * 256 : buf * G::ACC_OFF);
+                    for (int j = 0; j < nk; ++j) {
+                        const uint64_t da = sdesc_kmajor_sw128(a + j * kStepK), db = sdesc_kmajor_sw128(b + j * kStepK);
+                        const uint32_t accumulate = (j > 0 || (kt > 0 && !(kChains && kt == second))) ? 1u : 0u;
+                        if constexpr (kFp4) {
+                            const uint32_t sfa = tmem + G::SF_BASE + j * G::SF_STEP, sfb = sfa + 4;
+                            const uint32_t src = b + G::B_BYTES + j * kAtomBytes;
+                            cp_scale_atom_pair(sfa, sdesc_scale_atom(src));
+                            cp_scale_atom_pair(sfb, sdesc_scale_atom(src + G::SFA_BYTES));
+                            if (shift == 0)
+                                cp_scale_atom_pair(sfb + 4, sdesc_scale_atom(src + G::SFA_BYTES + kAtoms * kAtomBytes));
+                            mma_nvf4_pair(acc, da, db, idesc, sfa, sfb, accumulate);
+                        } else {
+                            mma_fp8_pair(acc, da, db, idesc, accumulate);
                         }
                     }
-                    if (!ok) break;
-                    mma_commit_pair(smem_u32(&acc_full[buf]));
-                    mma_commit_pair(peer_acc_full + buf * 8);
+                    mma_commit_pair(smem_u32(&empty[stage]));
+                    mma_commit_pair(peer_empty + stage * 8);
+                    if (++stage == G::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
+                if (!ok) break;
+                mma_commit_pair(smem_u32(&acc_full[buf]));
+                mma_commit_pair(peer_acc_full + buf * 8);
             }
             if (!ok) {
                 mma_commit_pair(smem_u32(drained));
@@ -336,62 +319,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
     } else {
         // ---------------------------------------------------------- epilogue --
         const int q = warp & 3, part = (warp - 2) >> 2;   // lane quarter, share of the columns
+        const EpiArgs& e = args.epi;
         float* s = scales + (warp - 2) * G::EPI_COLS;
         const float whole = kFp4 ? __fmul_rn(*args.sA, *args.sB) : 0.0f;
         int local = 0;
-        bool ok = true;
-        for (int u = pair; u < num_units && ok; u += npairs) {
+        for (int u = pair; u < num_units; u += npairs, ++local) {
             const Unit w = unit_of(u);
-            const int m_tile = w.m0, rounds = 4 >> w.shift;
+            const int buf = kChains ? 0 : local & 1, m_tile = w.m0;
             const int n = w.n_idx * 256 + rank * 128 + q * 32 + lane;
-            for (int half = 0; half < kHalves; ++half, ++local) {
-                // the second half reads what this same thread has stored of the first
-                const EpiArgs& e = half ? args.epi_add : args.epi;
-                const int buf = kBoth ? 0 : local & 1;
-                // the i-th 16 columns of this warp; NVFP4: interleaved, whole tiles from the shared
-                // columns on
-                const int first = kFp4 && buf == 0 && w.shift == 0 ? G::ACC_OFF : 0;
-                auto column = [&](int i) {
-                    return kFp4 ? ((part + 4 * i) * 16 + first) & 255 : part * (G::EPI_COLS >> w.shift) + i * 16;
-                };
-                // everything that does not depend on the accumulator, before the wait for it
-                const float t = kFp4 ? whole : n < e.N ? args.sB[n] : 0.0f;
-                const float bias = e.bias && n < e.N ? e.bias[n] : 0.0f;
-                EpiResidual<16> cur, next;
-                cur.load(e, m_tile + column(0), n);
-                if constexpr (!kFp4) stage_token_scales(args.sA, e.M, m_tile + column(0), G::EPI_COLS, s, lane);
-                // the warp stays together whichever of its lanes saw the budget run out
-                ok = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_full[buf], (kBoth ? local : local >> 1) & 1, err,
-                                                               kErrTimeoutEpi));
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * G::ACC_OFF;
-                // the round after which this warp has read all that the next tile may overwrite
-                const int last_shared = kFp4 && w.shift == 0 ? (G::SHARED - 1 - part) / 4 : rounds - 1;
+            // the i-th 16 columns of this warp; NVFP4: interleaved, whole tiles from the shared
+            // columns on
+            const int first = kFp4 && buf == 0 && w.shift == 0 ? G::ACC_OFF : 0;
+            auto column = [&](int i) {
+                return kFp4 ? ((part + 4 * i) * 16 + first) & 255 : part * (G::EPI_COLS >> w.shift) + i * 16;
+            };
+            const int rounds = 4 >> w.shift;
+            // everything that does not depend on the accumulator, before the wait for it
+            const float t = kFp4 ? whole : n < e.N ? args.sB[n] : 0.0f;
+            const float bias = e.bias && n < e.N ? e.bias[n] : 0.0f;
+            EpiResidual<16> cur, next;
+            cur.load(e, m_tile + column(0), n);
+            if constexpr (!kFp4) stage_token_scales(args.sA, e.M, m_tile + column(0), G::EPI_COLS, s, lane);
+            // the warp stays together whichever of its lanes saw the budget run out
+            if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_full[buf], (kChains ? local : local >> 1) & 1, err, kErrTimeoutEpi))) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * G::ACC_OFF;
+            // the round after which this warp has read all that the next tile may overwrite
+            const int last_shared = kFp4 && w.shift == 0 ? (G::SHARED - 1 - part) / 4 : rounds - 1;
 #pragma unroll 1
-                for (int i = 0; i < rounds; ++i) {
-                    uint32_t acc[16];
-                    const int c = column(i);
-                    tmem_ld_32x32b_x16(taddr + c, acc);
-                    if constexpr (kBoth) {
-                        uint32_t second[16];
-                        tmem_ld_32x32b_x16(taddr + 256 + c, second);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            acc[j] = __float_as_uint(__uint_as_float(acc[j]) + __uint_as_float(second[j]));
-                    }
-                    if (i + 1 < rounds) next.load(e, m_tile + column(i + 1), n);
+            for (int i = 0; i < rounds; ++i) {
+                uint32_t acc[16];
+                const int c = column(i);
+                tmem_ld_32x32b_x16(taddr + c, acc);
+                if constexpr (kChains) {
+                    uint32_t second[16];
+                    tmem_ld_32x32b_x16(taddr + 256 + c, second);
                     tmem_wait_ld();
-                    if (i == last_shared) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&acc_free[kOneSignal ? 0 : buf]), 0));
-                    }
-                    epilogue_store<16, !kFp4>(e, m_tile + c, n, acc, cur, s + i * 16, t, bias);
-                    cur = next;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        acc[j] = __float_as_uint(__uint_as_float(acc[j]) + __uint_as_float(second[j]));
                 }
+                if (i + 1 < rounds) next.load(e, m_tile + column(i + 1), n);
+                tmem_wait_ld();
+                if (i == last_shared) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&acc_free[kOneSignal ? 0 : buf]), 0));
+                }
+                epilogue_store<16, !kFp4>(e, m_tile + c, n, acc, cur, s + i * 16, t, bias);
+                cur = next;
             }
         }
     }
@@ -643,7 +619,7 @@ nvfp4_status operand_maps(const Operand& o, int box_rows, CUtensorMap* codes, CU
     return s;
 }
 
-template <bool kFp4, Chains kChains>
+template <bool kFp4, bool kChains>
 nvfp4_status launch_pair(const Operand& X, const Operand& W, const FusedArgs& args, cudaStream_t st) {
     using G = Pair<kFp4>;
     Maps maps = {};
@@ -679,13 +655,6 @@ nvfp4_status launch_pair(const Operand& X, const Operand& W, const FusedArgs& ar
     const int64_t most = resident[dev].load(std::memory_order_relaxed);
     const int64_t left = tiles % most;
     FusedArgs a = args;
-    if (kChains == kThroughOutput) {
-        a.epi_add = a.epi;
-        a.epi_add.bias = nullptr;
-        a.epi_add.res = a.epi.out;
-        a.epi_add.res_dtype = a.epi.out_dtype;
-        a.epi_add.ld_res = a.epi.ldc;
-    }
     a.tail_shift = !kFp4 && left * 4 <= most ? 2 : left * 2 <= most ? 1 : 0;
     a.tail_from = static_cast<int>(tiles - left);
     if (a.tail_shift && left) {
@@ -742,9 +711,9 @@ nvfp4_status launch_split(int split, const Operand& X, const Operand& W, const F
 // float64 its error grows in proportion to the number of steps (K = 5120, 160 steps:
 // 9.6e-7 of the result's norm in one chain, 4.2e-7 in two, 1.9e-7 in four), and 30 tiles
 // (K = 3840) keep it under 7.5e-7.  A bf16 result's own rounding is 1.7e-3.  In the pair
-// kernel (8192 x 12352 x 5120 in a loop: one chain 440 us) the first chain's sum waits in
-// the result, 459 us; with an activation it waits in the other accumulator, 484 us.
-// (Three stages and that sum in shared memory: three stages alone take 543.)
+// kernel two chains cost the overlap of a tile's epilogue with the next tile's products
+// (8192 x 12352 x 5120: 484 us against 440 in a loop; three stages and the first chain's
+// sum in shared memory instead would have kept it, but three stages alone take 543).
 constexpr int kChainTiles = 30;
 
 // The pair kernel from 32 tiles of 256 x 256 on, when there are more than 128 tokens
@@ -766,9 +735,8 @@ nvfp4_status fused_launch(const Operand& X, const Operand& W, const FusedArgs& a
     if (M > 128 && pair_tiles >= 32) {
         if constexpr (!kFp4)
             if (args.epi.out_dtype == NVFP4_DTYPE_FP32 && num_kt >= kChainTiles)
-                return args.epi.act == GEMM_ACT_NONE ? launch_pair<false, kThroughOutput>(X, W, args, st)
-                                                     : launch_pair<false, kBothAccumulators>(X, W, args, st);
-        return launch_pair<kFp4, kOneChain>(X, W, args, st);
+                return launch_pair<false, true>(X, W, args, st);
+        return launch_pair<kFp4, false>(X, W, args, st);
     }
     const int64_t n_tiles = (N + 127) / 128, most = num_sms() * 3 / 2;
     const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
