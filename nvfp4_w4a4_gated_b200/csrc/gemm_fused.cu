@@ -712,8 +712,10 @@ nvfp4_status launch_split(int split, const Operand& X, const Operand& W, const F
 // 9.6e-7 of the result's norm in one chain, 4.2e-7 in two, 1.9e-7 in four), and 30 tiles
 // (K = 3840) keep it under 7.5e-7.  A bf16 result's own rounding is 1.7e-3.  In the pair
 // kernel two chains cost the overlap of a tile's epilogue with the next tile's products
-// (8192 x 12352 x 5120: 484 us against 440 in a loop; three stages and the first chain's
-// sum in shared memory instead would have kept it, but three stages alone take 543).
+// (8192 x 12352 x 5120 under a steady load: 494 us, one chain 467).  Leaving the first
+// chain's sum in the result instead keeps the overlap, but under the power limit the
+// extra traffic costs more (517); three stages and that sum in shared memory: three stages
+// alone take 20 % more.
 constexpr int kChainTiles = 30;
 
 // The pair kernel from 32 tiles of 256 x 256 on, when there are more than 128 tokens

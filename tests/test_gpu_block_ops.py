@@ -271,6 +271,11 @@ def test_w8a8_long_sums(cuda_dev, M, N, K, act, res):
     done()
     # each chain has half the steps: half the bound
     check_product(C, value(A), value(B), 64, bias, act, r)
+    stream = rand((M, N), 10, F32, pad=3)
+    before = stream.clone()
+    nv.w8a8_gemm(A, B, bias=bias, act=act, residual=stream, out=stream)
+    done()
+    check_product(stream, value(A), value(B), 64, bias, act, before)
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 515, 256), (40, 1027, 1040), (200, 333, 256), (2300, 2311, 208)])
