@@ -245,6 +245,8 @@ SHAPES = [(1, 1, 16), (1, 128, 128), (1, 5120, 4096), (2, 129, 48), (16, 1000, 1
           (33, 640, 512), (64, 12352, 5120), (64, 128, 8192), (65, 130, 144), (128, 512, 1024), (129, 700, 272),
           (500, 333, 640), (257, 12352, 272), (2300, 2311, 208), (2304, 2304, 128), (2100, 2500, 16), (4000, 1300, 1040),
           (1237, 4099, 1040),
+          # K in three and in four
+          (64, 5120, 2064), (50, 6000, 1552), (128, 2000, 2000), (100, 5003, 1600), (40, 300, 2000), (9, 2000, 2064),
           # last rounds cut into narrow tiles, some of them past the last token
           (1030, 4099, 272), (1537, 1500, 128), (5000, 2000, 48)]
 
@@ -351,7 +353,8 @@ def nvfp4_value(t):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 1, 64), (1, 5120, 4096), (64, 1003, 320), (130, 515, 256), (300, 12352, 192),
-                                   (2300, 2311, 448), (1030, 4099, 320), (1537, 1500, 192), (5000, 2000, 64)])
+                                   (2300, 2311, 448), (1030, 4099, 320), (1537, 1500, 192), (5000, 2000, 64), (100, 3000, 4096),
+                                   (64, 5120, 4096), (50, 300, 4160), (9, 2000, 4160)])
 @pytest.mark.parametrize("bias,act,res", [(False, nv.ACT_NONE, None), (True, nv.ACT_SILU, F32), (True, nv.ACT_GELU, BF16)])
 def test_w4a4_fused(cuda_dev, M, N, K, bias, act, res):
     A = nv.nvfp4_quantize(rand((M, K), 41))
