@@ -12,8 +12,8 @@
 // What bounds it is the number of instructions per element: without its stores an
 // earlier form (24 instructions) took 71 of 80 us on 8192 x 12352 outputs, where the
 // products of K = 128 alone took 15.  Hence the arithmetic in pairs (one f32x2
-// instruction for two tokens), row addresses as base + j * (32-bit pitch), which is one
-// multiply-add each, and no test per token in whole chunks.
+// instruction for two tokens), running row pointers (base + j * pitch for each took up to
+// 7 % longer), and no test per token in whole chunks.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -133,7 +133,10 @@ struct EpiResidual {
     __device__ __forceinline__ void load_rows(const char* row, uint32_t pitch, int last) {
         if (last >= C - 1) {
 #pragma unroll
-            for (uint32_t j = 0; j < C; ++j) raw[j] = *reinterpret_cast<const T*>(row + static_cast<uint64_t>(j) * pitch);
+            for (uint32_t j = 0; j < C; ++j) {
+                raw[j] = *reinterpret_cast<const T*>(row);
+                row += pitch;
+            }
         } else {
 #pragma unroll
             for (uint32_t j = 0; j < C; ++j)
@@ -170,14 +173,18 @@ __device__ __forceinline__ void epilogue_store(const EpiArgs& e, int m0, int n, 
     F2 v[P];
     const F2 t2 = f2(t, t), b2 = f2(bias, bias);
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-        v[j] = f2(__uint_as_float(acc[2 * j]), __uint_as_float(acc[2 * j + 1]));
-        if constexpr (kTokenScales) {
-            const float2 sj = *reinterpret_cast<const float2*>(s + 2 * j);
+    for (int j = 0; j < P; ++j) v[j] = f2(__uint_as_float(acc[2 * j]), __uint_as_float(acc[2 * j + 1]));
+    if constexpr (kTokenScales) {
+        static_assert(C % 4 == 0, "token scales are read four at a time");
+#pragma unroll
+        for (int j = 0; j < P; j += 2) {
+            const float4 sj = *reinterpret_cast<const float4*>(s + 2 * j);
             v[j] = v[j] * f2(sj.x, sj.y);
+            v[j + 1] = v[j + 1] * f2(sj.z, sj.w);
         }
-        v[j] = fma(v[j], t2, b2);
     }
+#pragma unroll
+    for (int j = 0; j < P; ++j) v[j] = fma(v[j], t2, b2);
     if (e.act == GEMM_ACT_SILU) {
 #pragma unroll
         for (int j = 0; j < P; ++j) v[j] = silu(v[j]);
@@ -207,8 +214,9 @@ __device__ __forceinline__ void epilogue_store(const EpiArgs& e, int m0, int n, 
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(y), "f"(x));
         }
         auto put = [&](uint32_t j) {
-            *reinterpret_cast<uint16_t*>(row + static_cast<uint64_t>(j) * e.ldc) =
+            *reinterpret_cast<uint16_t*>(row) =
                 static_cast<uint16_t>(j & 1 ? w[j / 2] >> 16 : w[j / 2] & 0xFFFFu);
+            row += e.ldc;
         };
         store_rows<C>(count, put);
     } else {
@@ -216,7 +224,10 @@ __device__ __forceinline__ void epilogue_store(const EpiArgs& e, int m0, int n, 
         float x[C];
 #pragma unroll
         for (int j = 0; j < P; ++j) split(v[j], x[2 * j], x[2 * j + 1]);
-        auto put = [&](uint32_t j) { *reinterpret_cast<float*>(row + static_cast<uint64_t>(j) * e.ldc) = x[j]; };
+        auto put = [&](uint32_t j) {
+            *reinterpret_cast<float*>(row) = x[j];
+            row += e.ldc;
+        };
         store_rows<C>(count, put);
     }
 }
