@@ -8,6 +8,7 @@ raises.  PyTorch is used only to own device memory and to name the stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import math
@@ -364,19 +365,32 @@ def w4a4_gemm(A: NVFP4Matrix, B: NVFP4Matrix, C: torch.Tensor | None = None, str
     return C
 
 
-def _used_on(stream, *tensors):
-    """Tensors made here for a given stream: their memory is not reused before it is done."""
+_CURRENT = contextlib.nullcontext()
+
+
+def _pool(stream):
+    """The context in which a call on a given stream makes new tensors.  Their memory is
+    that stream's: a block freed on the current stream may still be in use there, and
+    nothing orders ``stream`` behind that use."""
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
+
+
+def _used_here(stream, *tensors):
+    """Tensors made for a given stream go to the caller, whose current stream may read
+    them: their memory is not reused before it is done."""
     if stream is not None:
+        here = torch.cuda.current_stream(stream.device)
         for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+            t.record_stream(here)
 
 
-def _new_fp8(x, scale, stream):
-    """A new FP8Matrix shaped like x, around ``scale``, and its C form."""
-    codes = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
+def _new_fp8(x, like, stream):
+    """A new FP8Matrix shaped like x, on ``like``'s device, and its C form."""
     rows, cols = x.shape
-    _used_on(stream, codes, scale)
+    with _pool(stream):
+        codes = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
+        scale = like.new_empty(rows, dtype=torch.float32)
+    _used_here(stream, codes, scale)
     return FP8Matrix(codes, scale), _Fp8(codes.data_ptr(), scale.data_ptr(), rows, cols, cols)
 
 
@@ -384,7 +398,7 @@ def fp8_quantize(x: torch.Tensor, out: FP8Matrix | None = None, stream=None) -> 
     """Quantise the rows of a bf16 or fp32 CUDA matrix to E4M3 codes with one scale a row."""
     ptr, rows, cols, ld, dtype, dev = _rows(x, "x")
     if out is None:
-        out, q = _new_fp8(x, x.new_empty(rows, dtype=torch.float32), stream)
+        out, q = _new_fp8(x, x, stream)
     else:
         q = out.c(x.shape, dev)
     _on(dev, stream, lib().fp8_quantize, ptr, dtype, rows, cols, ld, ctypes.byref(q))
@@ -407,9 +421,10 @@ def add_rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, residual: torch.Tenso
     if residual is not None:
         r_ptr, _, _, r_ld, r_dtype, _ = _rows(residual, "residual", _DTYPES, shape, dev)
         if h is None:
-            h = torch.empty_like(residual, memory_format=torch.contiguous_format)
+            with _pool(stream):
+                h = torch.empty_like(residual, memory_format=torch.contiguous_format)
             h_ptr, h_ld = h.data_ptr(), cols
-            _used_on(stream, h)
+            _used_here(stream, h)
         else:
             h_ptr, _, _, h_ld, h_dtype, _ = _rows(h, "h", _DTYPES, shape, dev)
             if h_dtype != r_dtype:
@@ -419,16 +434,17 @@ def add_rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, residual: torch.Tenso
     if out is not None:
         q = ctypes.byref(out.c(shape, dev))
     elif want_fp8:
-        out, q = _new_fp8(x, w.new_empty(rows), stream)
+        out, q = _new_fp8(x, w, stream)
         q = ctypes.byref(q)
     if norm is not None:
         n_ptr, _, _, n_ld, n_dtype, _ = _rows(norm, "norm", _DTYPES, shape, dev)
         if n_dtype != DTYPE_BF16:
             raise ValueError("norm is bfloat16")
     elif want_norm:
-        norm = torch.empty_like(x, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
+        with _pool(stream):
+            norm = torch.empty_like(x, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
         n_ptr, n_ld = norm.data_ptr(), cols
-        _used_on(stream, norm)
+        _used_here(stream, norm)
     if amax_word is not None:
         if amax_word.get_device() != dev or amax_word.element_size() != 4 or amax_word.numel() < 1:
             raise ValueError("amax_word: a 32-bit word on x's device is expected")
@@ -444,9 +460,10 @@ def _epilogue(M: int, N: int, like, dev: int, bias, act: int, residual, out, out
         o_dtype = _DTYPES.get(out_dtype)
         if o_dtype is None:
             raise ValueError(f"out_dtype {out_dtype}: bfloat16 or float32 is expected")
-        out = like.new_empty(shape, dtype=out_dtype)
+        with _pool(stream):
+            out = like.new_empty(shape, dtype=out_dtype)
         o_ptr, ldc = out.data_ptr(), N
-        _used_on(stream, out)
+        _used_here(stream, out)
     else:
         o_ptr, _, _, ldc, o_dtype, _ = _rows(out, "out", _DTYPES, shape, dev)
     r_ptr, r_dtype, r_ld = None, 0, 0

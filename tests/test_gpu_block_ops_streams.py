@@ -1,0 +1,77 @@
+"""Block operators called with ``stream=``: their new tensors are ordered with that stream.
+
+A sleep on the current stream keeps work on a freed block pending while the call on the
+other stream runs, so results that shared the block would be overwritten by it."""
+import pytest
+import torch
+
+import nvfp4_w4a4_gated_b200 as nv
+
+pytestmark = pytest.mark.gpu
+
+SLEEP = 200_000_000   # clocks, about 0.1 s
+
+
+def calls():
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((1000, 4096), generator=g, device="cuda")
+    r = torch.randn((1000, 4096), generator=g, device="cuda").bfloat16()
+    w = torch.randn(4096, generator=g, device="cuda")
+    A, B = nv.fp8_quantize(x), nv.fp8_quantize(x + 1)
+    A4, B4 = nv.nvfp4_quantize(x), nv.nvfp4_quantize(x + 1)
+
+    def quantize(**kw):
+        q = nv.fp8_quantize(x, **kw)
+        return q.codes, q.scale
+
+    def norm(**kw):
+        h, q, n = nv.add_rmsnorm_quantize(x, w, residual=r, want_norm=True, **kw)
+        return h, q.codes, q.scale, n
+
+    return {"quantize": quantize, "norm": norm, "w8a8": lambda **kw: (nv.w8a8_gemm(A, B, **kw),),
+            "w4a4": lambda **kw: (nv.w4a4_gemm_fused(A4, B4, **kw),)}
+
+
+def equal(a, b):
+    return all(torch.equal(s.view(torch.uint8), t.view(torch.uint8)) for s, t in zip(a, b, strict=True))
+
+
+@pytest.mark.parametrize("name", ["quantize", "norm", "w8a8", "w4a4"])
+def test_memory_freed_on_the_current_stream(cuda_dev, name):
+    call = calls()[name]
+    want = call()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    call(stream=s)   # first launches are over
+    torch.cuda.synchronize()
+    busy = [torch.empty_like(t) for t in want]
+    torch.cuda._sleep(SLEEP)
+    for t in busy:
+        t.view(torch.uint8).fill_(0x35)
+    at = {t.data_ptr() for t in busy}
+    del busy, t   # free for this stream's next tensors, with the fills still to run
+    assert {torch.empty_like(t).data_ptr() for t in want} & at
+    got = call(stream=s)
+    torch.cuda.synchronize()
+    nv.check_device_error()
+    assert equal(got, want)
+
+
+@pytest.mark.parametrize("name", ["quantize", "norm", "w8a8", "w4a4"])
+def test_result_read_on_the_current_stream_and_dropped(cuda_dev, name):
+    call = calls()[name]
+    want = call()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = call(stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda._sleep(SLEEP)
+    kept = [t.clone() for t in got]
+    del got
+    with torch.cuda.stream(s):   # the stream's next tensors of these sizes
+        after = [torch.empty_like(t) for t in want]
+        for t in after:
+            t.view(torch.uint8).fill_(0x35)
+    torch.cuda.synchronize()
+    nv.check_device_error()
+    assert equal(kept, want)
