@@ -241,6 +241,25 @@ def _on(dev: int, stream, call, *args):
         _check(status)
 
 
+_CURRENT = contextlib.nullcontext()
+
+
+def _pool(stream):
+    """The context in which a call on a given stream makes new tensors.  Their memory is
+    that stream's: a block freed on the current stream may still be in use there, and
+    nothing orders ``stream`` behind that use."""
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
+
+
+def _used_here(stream, *tensors):
+    """Tensors made for a given stream go to the caller, whose current stream may read
+    them: their memory is not reused before it is done."""
+    if stream is not None:
+        here = torch.cuda.current_stream(stream.device)
+        for t in tensors:
+            t.record_stream(here)
+
+
 # ------------------------------------------------------------------ tensors --
 @dataclasses.dataclass
 class NVFP4Matrix:
@@ -344,12 +363,14 @@ def nvfp4_quantize(x: torch.Tensor, out: NVFP4Matrix | None = None, given_scale:
     assert x.is_cuda and x.dim() == 2 and x.stride(1) == 1
     dtype = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}[x.dtype]
     rows, cols = x.shape
-    if out is None:
-        out = NVFP4Matrix.empty(rows, cols, x.device)
-    if workspace is None:
-        workspace = _scratch(lib().nvfp4_quantize_workspace_size(), x.device)
     if mode is None:
         mode = QUANT_GIVEN_SCALE if given_scale else QUANT_COMPUTE_SCALE
+    if out is None:
+        with _pool(stream):
+            out = NVFP4Matrix.empty(rows, cols, x.device)
+        _used_here(stream, out.codes, out.sf, out.scale)
+    if workspace is None:
+        workspace = _scratch(lib().nvfp4_quantize_workspace_size(), x.device)
     t = out.c()
     _check(lib().nvfp4_quantize(_ptr(x), dtype, rows, cols, x.stride(0), ctypes.byref(t), mode, _ptr(workspace),
                                 workspace.numel(), _stream(stream)))
@@ -359,29 +380,12 @@ def nvfp4_quantize(x: torch.Tensor, out: NVFP4Matrix | None = None, given_scale:
 def w4a4_gemm(A: NVFP4Matrix, B: NVFP4Matrix, C: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """C = S_A S_B (A_hat @ B_hat^T), float32 [A.rows, B.rows]."""
     if C is None:
-        C = torch.empty((A.rows, B.rows), dtype=torch.float32, device=A.codes.device)
+        with _pool(stream):
+            C = torch.empty((A.rows, B.rows), dtype=torch.float32, device=A.codes.device)
+        _used_here(stream, C)
     ta, tb = A.c(), B.c()
     _check(lib().w4a4_gemm(ctypes.byref(ta), ctypes.byref(tb), _ptr(C), C.stride(0), _stream(stream)))
     return C
-
-
-_CURRENT = contextlib.nullcontext()
-
-
-def _pool(stream):
-    """The context in which a call on a given stream makes new tensors.  Their memory is
-    that stream's: a block freed on the current stream may still be in use there, and
-    nothing orders ``stream`` behind that use."""
-    return _CURRENT if stream is None else torch.cuda.stream(stream)
-
-
-def _used_here(stream, *tensors):
-    """Tensors made for a given stream go to the caller, whose current stream may read
-    them: their memory is not reused before it is done."""
-    if stream is not None:
-        here = torch.cuda.current_stream(stream.device)
-        for t in tensors:
-            t.record_stream(here)
 
 
 def _new_fp8(x, like, stream):
@@ -502,10 +506,12 @@ def gdn_gates(proj: torch.Tensor, dims: GdnDims, A_log: torch.Tensor, dt_bias: t
     """Returns (q_hat [n,Hk,K], k_hat [n,Hk,K], g [n,Hv], beta [n,Hv]) from the fused projection."""
     n = proj.shape[0]
     dev = proj.device
-    q_hat = torch.empty((n, dims.Hk, dims.K), dtype=torch.float32, device=dev)
-    k_hat = torch.empty_like(q_hat)
-    g = torch.empty((n, dims.Hv), dtype=torch.float32, device=dev)
-    beta = torch.empty_like(g)
+    with _pool(stream):
+        q_hat = torch.empty((n, dims.Hk, dims.K), dtype=torch.float32, device=dev)
+        k_hat = torch.empty_like(q_hat)
+        g = torch.empty((n, dims.Hv), dtype=torch.float32, device=dev)
+        beta = torch.empty_like(g)
+    _used_here(stream, q_hat, k_hat, g, beta)
     d = dims.c()
     _check(lib().gdn_gates(_ptr(proj), proj.stride(0), n, ctypes.byref(d), _ptr(A_log), _ptr(dt_bias), _ptr(q_hat),
                            _ptr(k_hat), _ptr(g), _ptr(beta), _stream(stream)))
@@ -518,7 +524,9 @@ def gdn_output_gate(o: torch.Tensor, z: torch.Tensor, w: torch.Tensor, out=None,
     w: [V].  Returns out (a new tensor unless given; may be o)."""
     n, Hv, V = o.shape
     if out is None:
-        out = torch.empty_like(o)
+        with _pool(stream):
+            out = torch.empty_like(o)
+        _used_here(stream, out)
     _check(lib().gdn_output_gate(_ptr(o), _ptr(z), z.stride(0), _ptr(w), n, Hv, V, _ptr(out), _ptr(amax_word),
                                  _stream(stream)))
     return out
@@ -531,7 +539,9 @@ def gdn_short_conv(x: torch.Tensor, w: torch.Tensor, B: int, T: int, out=None, s
     Returns out [B*T, C] (a new tensor unless given)."""
     C, W = w.shape
     if out is None:
-        out = torch.empty((B * T, C), dtype=torch.float32, device=x.device)
+        with _pool(stream):
+            out = torch.empty((B * T, C), dtype=torch.float32, device=x.device)
+        _used_here(stream, out)
     _check(lib().gdn_short_conv(_ptr(x), x.stride(0), B, T, C, W, _ptr(w), _ptr(state_in), _ptr(state_out), _ptr(out),
                                 out.stride(0), _stream(stream)))
     return out
@@ -546,11 +556,14 @@ def gdn_scan(q_hat, k_hat, v, g, beta, B: int, T: int, dims: GdnDims, scale: flo
     if scale is None:
         scale = 1.0 / math.sqrt(dims.K)
     if o is None:
-        o = torch.empty((B * T, dims.Hv, dims.V), dtype=torch.float32, device=dev)
+        with _pool(stream):
+            o = torch.empty((B * T, dims.Hv, dims.V), dtype=torch.float32, device=dev)
+        _used_here(stream, o)
     d = dims.c()
     need = lib().gdn_scan_workspace_size(B, T, ctypes.byref(d), algo)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        with _pool(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ld_v = v.stride(0)
     _check(lib().gdn_scan(_ptr(q_hat), _ptr(k_hat), _ptr(v), ld_v, _ptr(g), _ptr(beta), B, T, ctypes.byref(d),
                           float(scale), form, algo, _ptr(state_in), _ptr(state_out), _ptr(o), _ptr(workspace),
@@ -568,13 +581,18 @@ def gdn_scan_transition(q_hat, k_hat, g, beta, B: int, T: int, dims: GdnDims, sc
     if scale is None:
         scale = 1.0 / math.sqrt(dims.K)
     if P is None:
-        P = torch.empty((B, dims.Hv, dims.K, dims.K), dtype=torch.float32, device=dev)
+        with _pool(stream):
+            P = torch.empty((B, dims.Hv, dims.K, dims.K), dtype=torch.float32, device=dev)
+        _used_here(stream, P)
     if qmap is None:
-        qmap = torch.empty((B * T, dims.Hv, dims.K), dtype=torch.float32, device=dev)
+        with _pool(stream):
+            qmap = torch.empty((B * T, dims.Hv, dims.K), dtype=torch.float32, device=dev)
+        _used_here(stream, qmap)
     d = dims.c()
     need = lib().gdn_scan_transition_workspace_size(B, T, ctypes.byref(d), algo)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        with _pool(stream):
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     _check(lib().gdn_scan_transition(_ptr(q_hat), _ptr(k_hat), _ptr(g), _ptr(beta), B, T, ctypes.byref(d),
                                      float(scale), form, algo, _ptr(P), _ptr(qmap), _ptr(workspace),
                                      workspace.numel(), _stream(stream)))
@@ -591,7 +609,9 @@ def gdn_state_combine(P, S_loc, S_in, out=None, stream=None):
     m = P.numel() // (n * K * K)
     V = (S_in if S_in is not None else S_loc).shape[-1]
     if out is None:
-        out = torch.empty((B, Hv, K, V), dtype=torch.float32, device=P.device)
+        with _pool(stream):
+            out = torch.empty((B, Hv, K, V), dtype=torch.float32, device=P.device)
+        _used_here(stream, out)
     _check(lib().gdn_state_combine(_ptr(P), _ptr(S_loc), _ptr(S_in), _ptr(out), m, n, K, V, _stream(stream)))
     return out
 
@@ -604,14 +624,17 @@ def gdn_scan_span(q_hat, k_hat, v, g, beta, B: int, T: int, dims: GdnDims, scale
     if scale is None:
         scale = 1.0 / math.sqrt(dims.K)
     f32 = dict(dtype=torch.float32, device=dev)
-    o = torch.empty((B * T, dims.Hv, dims.V), **f32)
-    S_loc = torch.empty((B, dims.Hv, dims.K, dims.V), **f32)
-    P = torch.empty((B, dims.Hv, dims.K, dims.K), **f32)
-    qmap = torch.empty((B * T, dims.Hv, dims.K), **f32)
+    with _pool(stream):
+        o = torch.empty((B * T, dims.Hv, dims.V), **f32)
+        S_loc = torch.empty((B, dims.Hv, dims.K, dims.V), **f32)
+        P = torch.empty((B, dims.Hv, dims.K, dims.K), **f32)
+        qmap = torch.empty((B * T, dims.Hv, dims.K), **f32)
+    _used_here(stream, o, S_loc, P, qmap)
     d = dims.c()
     need = lib().gdn_scan_span_workspace_size(B, T, ctypes.byref(d), algo)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        with _pool(stream):
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     _check(lib().gdn_scan_span(_ptr(q_hat), _ptr(k_hat), _ptr(v), v.stride(0), _ptr(g), _ptr(beta), B, T,
                                ctypes.byref(d), float(scale), form, algo, _ptr(o), _ptr(S_loc), _ptr(P), _ptr(qmap),
                                _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -635,7 +658,9 @@ def gdn_scan_noalloc(q_hat, k_hat, v, g, beta, B: int, T: int, dims: GdnDims, sc
     if scale is None:
         scale = 1.0 / math.sqrt(dims.K)
     if o is None:
-        o = torch.empty((B * T, dims.Hv, dims.V), dtype=torch.float32, device=dev)
+        with _pool(stream):
+            o = torch.empty((B * T, dims.Hv, dims.V), dtype=torch.float32, device=dev)
+        _used_here(stream, o)
     d = dims.c()
     _check(lib().gdn_scan_noalloc(_ptr(q_hat), _ptr(k_hat), _ptr(v), v.stride(0), _ptr(g), _ptr(beta), B, T,
                                   ctypes.byref(d), float(scale), form, _ptr(state_in), _ptr(state_out), _ptr(o),
@@ -659,11 +684,15 @@ def gdn_layer_forward(w: LayerWeights, x: torch.Tensor, B: int, T: int, y=None, 
     events: optional list of 7 torch.cuda.Event (timing enabled), recorded on the
     stream around the layer's stages (gdn_layer_forward_timed)."""
     assert x.dtype == torch.bfloat16 and x.is_contiguous()
-    if y is None:
-        y = torch.empty((B * T, w.hidden), dtype=torch.float32, device=x.device)
     lay = layer_workspace_layout(w, B, T)
+    if y is None:
+        with _pool(stream):
+            y = torch.empty((B * T, w.hidden), dtype=torch.float32, device=x.device)
+        _used_here(stream, y)
     if workspace is None:
-        workspace = torch.empty(lay["total"], dtype=torch.uint8, device=x.device)
+        with _pool(stream):
+            workspace = torch.empty(lay["total"], dtype=torch.uint8, device=x.device)
+        _used_here(stream, workspace)
     lw = w.c()
     if events is not None:
         if len(events) != 7:

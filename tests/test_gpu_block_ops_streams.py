@@ -1,4 +1,4 @@
-"""Block operators called with ``stream=``: their new tensors are ordered with that stream.
+"""Calls with ``stream=``: their new tensors are ordered with that stream.
 
 A sleep on the current stream keeps work on a freed block pending while the call on the
 other stream runs, so results that shared the block would be overwritten by it."""
@@ -28,7 +28,21 @@ def calls():
         h, q, n = nv.add_rmsnorm_quantize(x, w, residual=r, want_norm=True, **kw)
         return h, q.codes, q.scale, n
 
-    return {"quantize": quantize, "norm": norm, "w8a8": lambda **kw: (nv.w8a8_gemm(A, B, **kw),),
+    def nvfp4(**kw):
+        q = nv.nvfp4_quantize(x, **kw)
+        return q.codes, q.sf, q.scale
+
+    dims, T = nv.GdnDims(2, 4, 128, 128), 256
+    proj = torch.randn((T, dims.n_in), generator=g, device="cuda")
+    A_log, dt = torch.zeros(4, device="cuda"), torch.zeros(4, device="cuda")
+    gates = nv.gdn_gates(proj, dims, A_log, dt)
+    v = proj[:, 512:]
+
+    def scan(**kw):   # with a workspace that is dropped when the call returns
+        return nv.gdn_scan(gates[0], gates[1], v, gates[2], gates[3], 1, T, dims, algo=nv.SCAN_CHUNKED, **kw)[:1]
+
+    return {"nvfp4": nvfp4, "gemm": lambda **kw: (nv.w4a4_gemm(A4, B4, **kw),), "scan": scan,
+            "gates": lambda **kw: nv.gdn_gates(proj, dims, A_log, dt, **kw), "quantize": quantize, "norm": norm, "w8a8": lambda **kw: (nv.w8a8_gemm(A, B, **kw),),
             "w4a4": lambda **kw: (nv.w4a4_gemm_fused(A4, B4, **kw),)}
 
 
@@ -36,7 +50,7 @@ def equal(a, b):
     return all(torch.equal(s.view(torch.uint8), t.view(torch.uint8)) for s, t in zip(a, b, strict=True))
 
 
-@pytest.mark.parametrize("name", ["quantize", "norm", "w8a8", "w4a4"])
+@pytest.mark.parametrize("name", ["quantize", "norm", "w8a8", "w4a4", "nvfp4", "gemm", "scan", "gates"])
 def test_memory_freed_on_the_current_stream(cuda_dev, name):
     call = calls()[name]
     want = call()
@@ -57,7 +71,7 @@ def test_memory_freed_on_the_current_stream(cuda_dev, name):
     assert equal(got, want)
 
 
-@pytest.mark.parametrize("name", ["quantize", "norm", "w8a8", "w4a4"])
+@pytest.mark.parametrize("name", ["quantize", "norm", "w8a8", "w4a4", "nvfp4", "gemm", "scan", "gates"])
 def test_result_read_on_the_current_stream_and_dropped(cuda_dev, name):
     call = calls()[name]
     want = call()
