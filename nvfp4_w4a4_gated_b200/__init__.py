@@ -370,7 +370,14 @@ def nvfp4_quantize(x: torch.Tensor, out: NVFP4Matrix | None = None, given_scale:
             out = NVFP4Matrix.empty(rows, cols, x.device)
         _used_here(stream, out.codes, out.sf, out.scale)
     if workspace is None:
-        workspace = _scratch(lib().nvfp4_quantize_workspace_size(), x.device)
+        # the amax word that one call leaves for the next is kept; a call that only needs one
+        # itself has its own, so that calls on two streams or in two graphs share none
+        size = lib().nvfp4_quantize_workspace_size()
+        if mode in (QUANT_AMAX_ONLY, QUANT_FROM_AMAX):
+            workspace = _scratch(size, x.device)
+        else:
+            with _pool(stream):
+                workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
     t = out.c()
     _check(lib().nvfp4_quantize(_ptr(x), dtype, rows, cols, x.stride(0), ctypes.byref(t), mode, _ptr(workspace),
                                 workspace.numel(), _stream(stream)))

@@ -89,3 +89,43 @@ def test_result_read_on_the_current_stream_and_dropped(cuda_dev, name):
     torch.cuda.synchronize()
     nv.check_device_error()
     assert equal(kept, want)
+
+
+class Recorder:
+    """The library, with the workspace of each nvfp4_quantize noted."""
+
+    def __init__(self, real):
+        self.real, self.seen = real, []
+
+    def __getattr__(self, name):
+        return getattr(self.real, name)
+
+    def nvfp4_quantize(self, *args):
+        self.seen.append(args[7].value)
+        return self.real.nvfp4_quantize(*args)
+
+
+def test_quantisers_on_two_streams_or_in_two_graphs_share_no_amax_word(cuda_dev, monkeypatch):
+    x = torch.randn((300, 512), device="cuda")
+    want = nv.nvfp4_quantize(x)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    lib = Recorder(nv.lib())
+    monkeypatch.setattr(nv, "_lib", lib)
+    got = [nv.nvfp4_quantize(x, stream=s) for s in streams]
+    torch.cuda.synchronize()
+    assert len(set(lib.seen)) == 2
+    lib.seen.clear()
+    graphs = []
+    for _ in streams:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(nv.nvfp4_quantize(x))
+        graphs.append(g)
+    assert len(set(lib.seen)) == 2
+    for g in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    nv.check_device_error()
+    for q in got:
+        assert equal((q.codes, q.sf, q.scale), (want.codes, want.sf, want.scale))
