@@ -260,6 +260,14 @@ def _used_here(stream, *tensors):
             t.record_stream(here)
 
 
+def _made(stream, make, *args, **kwargs):
+    """make(...) for a call on a given stream."""
+    with _pool(stream):
+        t = make(*args, **kwargs)
+    _used_here(stream, t)
+    return t
+
+
 # ------------------------------------------------------------------ tensors --
 @dataclasses.dataclass
 class NVFP4Matrix:
@@ -398,10 +406,12 @@ def w4a4_gemm(A: NVFP4Matrix, B: NVFP4Matrix, C: torch.Tensor | None = None, str
 def _new_fp8(x, like, stream):
     """A new FP8Matrix shaped like x, on ``like``'s device, and its C form."""
     rows, cols = x.shape
-    with _pool(stream):
+    if stream is None:
         codes = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
         scale = like.new_empty(rows, dtype=torch.float32)
-    _used_here(stream, codes, scale)
+    else:
+        codes = _made(stream, torch.empty, (rows, cols), dtype=torch.float8_e4m3fn, device=x.device)
+        scale = _made(stream, torch.empty, rows, dtype=torch.float32, device=x.device)
     return FP8Matrix(codes, scale), _Fp8(codes.data_ptr(), scale.data_ptr(), rows, cols, cols)
 
 
@@ -432,10 +442,11 @@ def add_rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, residual: torch.Tenso
     if residual is not None:
         r_ptr, _, _, r_ld, r_dtype, _ = _rows(residual, "residual", _DTYPES, shape, dev)
         if h is None:
-            with _pool(stream):
+            if stream is None:
                 h = torch.empty_like(residual, memory_format=torch.contiguous_format)
+            else:
+                h = _made(stream, torch.empty_like, residual, memory_format=torch.contiguous_format)
             h_ptr, h_ld = h.data_ptr(), cols
-            _used_here(stream, h)
         else:
             h_ptr, _, _, h_ld, h_dtype, _ = _rows(h, "h", _DTYPES, shape, dev)
             if h_dtype != r_dtype:
@@ -452,10 +463,11 @@ def add_rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, residual: torch.Tenso
         if n_dtype != DTYPE_BF16:
             raise ValueError("norm is bfloat16")
     elif want_norm:
-        with _pool(stream):
+        if stream is None:
             norm = torch.empty_like(x, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
+        else:
+            norm = _made(stream, torch.empty, shape, dtype=torch.bfloat16, device=x.device)
         n_ptr, n_ld = norm.data_ptr(), cols
-        _used_here(stream, norm)
     if amax_word is not None:
         if amax_word.get_device() != dev or amax_word.element_size() != 4 or amax_word.numel() < 1:
             raise ValueError("amax_word: a 32-bit word on x's device is expected")
@@ -471,10 +483,9 @@ def _epilogue(M: int, N: int, like, dev: int, bias, act: int, residual, out, out
         o_dtype = _DTYPES.get(out_dtype)
         if o_dtype is None:
             raise ValueError(f"out_dtype {out_dtype}: bfloat16 or float32 is expected")
-        with _pool(stream):
-            out = like.new_empty(shape, dtype=out_dtype)
+        out = (like.new_empty(shape, dtype=out_dtype) if stream is None else
+               _made(stream, torch.empty, shape, dtype=out_dtype, device=like.device))
         o_ptr, ldc = out.data_ptr(), N
-        _used_here(stream, out)
     else:
         o_ptr, _, _, ldc, o_dtype, _ = _rows(out, "out", _DTYPES, shape, dev)
     r_ptr, r_dtype, r_ld = None, 0, 0
