@@ -285,8 +285,22 @@ class NVFP4Matrix:
                            torch.empty(sf_bytes, dtype=torch.uint8, device=device),
                            torch.empty(1, dtype=torch.float32, device=device), rows, cols)
 
-    def c(self) -> _Tensor:
-        return _Tensor(_dev_addr(self.codes), _dev_addr(self.sf), _dev_addr(self.scale), self.rows, self.cols)
+    def c(self, dev=None) -> _Tensor:
+        """The C form, after a check that the buffers hold a matrix of this size (on device ``dev``)."""
+        codes, sf, scale, rows, cols = self.codes, self.sf, self.scale, self.rows, self.cols
+        if codes.nbytes * 2 != rows * cols or not codes.is_contiguous():
+            raise ValueError(f"codes: {rows} x {cols // 2} contiguous bytes are expected")
+        if sf.nbytes < (rows + 127) // 128 * 128 * (cols // 16) or not sf.is_contiguous():
+            raise ValueError("sf: nvfp4_sf_bytes(rows, cols) contiguous bytes are expected")
+        if scale.dtype != torch.float32 or scale.nbytes < 4:
+            raise ValueError("scale: a float32 value is expected")
+        at = codes.get_device()
+        if at < 0:
+            _dev_addr(codes)
+        if sf.get_device() != at or scale.get_device() != at or (dev is not None and at != dev):
+            raise ValueError(f"codes, sf and scale are on {codes.device}, {sf.device} and {scale.device}, expected "
+                             f"cuda:{at if dev is None else dev}")
+        return _Tensor(codes.data_ptr(), sf.data_ptr(), scale.data_ptr(), rows, cols)
 
 
 @dataclasses.dataclass
@@ -511,10 +525,7 @@ def w4a4_gemm_fused(A: NVFP4Matrix, B: NVFP4Matrix, bias=None, act: int = ACT_NO
                     out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """act(A @ B^T + bias) + residual for NVFP4 operands; arguments as for w8a8_gemm."""
     dev = A.codes.get_device()
-    a, b = A.c(), B.c()
-    for t in (A.sf, A.scale, B.codes, B.sf, B.scale):
-        if t.get_device() != dev:
-            raise ValueError(f"an operand is on {t.device}, A's codes on cuda:{dev}")
+    a, b = A.c(), B.c(dev)
     out, e = _epilogue(A.rows, B.rows, A.codes, dev, bias, act, residual, out, out_dtype, stream)
     _on(dev, stream, lib().w4a4_gemm_fused, ctypes.byref(a), ctypes.byref(b), ctypes.byref(e))
     return out

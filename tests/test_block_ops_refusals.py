@@ -109,3 +109,33 @@ def test_host_tensors_are_refused():
     for call in (lambda: nv.fp8_quantize(x), lambda: nv.add_rmsnorm_quantize(x, w), lambda: nv.w8a8_gemm(q, q)):
         with pytest.raises(ValueError, match="CUDA tensors"):
             call()
+
+
+def nvfp4(rows=130, cols=128, codes=None, sf=None, scale=None):
+    return nv.NVFP4Matrix(torch.zeros((rows, cols // 2), dtype=torch.uint8) if codes is None else codes,
+                          torch.zeros(256 * cols // 16, dtype=torch.uint8) if sf is None else sf,
+                          torch.ones(1) if scale is None else scale, rows, cols)
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("codes", dict(codes=torch.zeros((129, 64), dtype=torch.uint8))),
+    ("codes", dict(codes=torch.zeros((130, 63), dtype=torch.uint8))),
+    ("codes", dict(codes=torch.zeros((130, 80), dtype=torch.uint8)[:, :64])),
+    ("codes", dict(codes=torch.zeros((64, 130), dtype=torch.uint8).t())),
+    ("codes", dict(codes=torch.zeros((1, 64), dtype=torch.uint8).expand(130, 64))),
+    ("codes", dict(codes=torch.zeros((130, 64), dtype=torch.int16))),
+    ("sf", dict(sf=torch.zeros(130 * 8, dtype=torch.uint8))),
+    ("sf", dict(sf=torch.zeros((256, 16), dtype=torch.uint8)[:, :8])),
+    ("sf", dict(sf=torch.zeros(256 * 8, dtype=torch.uint8)[::2])),
+    ("scale", dict(scale=torch.ones(1, dtype=torch.float64))),
+    ("scale", dict(scale=torch.ones(0))),
+])
+def test_nvfp4_buffers_that_do_not_hold_the_matrix(name, kw):
+    """Refused before the device is looked at, so host tensors show it."""
+    good, bad = nvfp4(), nvfp4(**kw)
+    for call in (lambda: nv.w4a4_gemm_fused(bad, good), lambda: nv.w4a4_gemm(bad, good, C=torch.zeros(130, 130)),
+                 lambda: bad.c()):
+        with pytest.raises(ValueError, match=name + ": .* expected"):
+            call()
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        good.c()

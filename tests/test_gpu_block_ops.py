@@ -15,6 +15,7 @@ Bounds, with u = 2^-24 (half a float32 step, relative):
   the two scales and the bias add 8 more such terms.  The activations' slopes are at most 1.13 and
   their own evaluation is within 8 u of the argument's magnitude.
 - an output: half a step of its type (bf16 2^-8, float32 2^-24)."""
+import dataclasses
 import math
 import subprocess
 import sys
@@ -624,4 +625,17 @@ def test_refused_tensors(cuda_dev):
     for call in refused:
         with pytest.raises((nv.NVFP4Error, ValueError)):
             call()
+    done()
+
+
+def test_refused_nvfp4_operands(cuda_dev):
+    A, B = nv.nvfp4_quantize(rand((4, 128), 97)), nv.nvfp4_quantize(rand((200, 128), 98))
+    def but(m, **kw):
+        return dataclasses.replace(m, **kw)
+    wrong = [(but(A, rows=8), B), (but(A, cols=256), but(B, cols=256)), (A, but(B, sf=B.sf[:1024])), (A, but(B, codes=B.codes[:128])),
+             (A, but(B, codes=B.codes.t())), (but(A, sf=A.sf.cpu()), B), (but(A, scale=A.scale.cpu()), B),
+             (A, but(B, codes=B.codes.cpu(), sf=B.sf.cpu(), scale=B.scale.cpu())), (A, but(B, scale=B.scale.double()))]
+    for a, b in wrong:
+        with pytest.raises(ValueError):
+            nv.w4a4_gemm_fused(a, b)
     done()
