@@ -351,6 +351,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
             for (int i = 0; i < rounds; ++i) {
                 uint32_t acc[16];
                 const int c = column(i);
+                // lanes past N take another path through the loads and stores of C and R, and
+                // TMEM instructions want the warp together
+                __syncwarp();
                 tmem_ld_32x32b_x16(taddr + c, acc);
                 if constexpr (kChains) {
                     uint32_t second[16];
@@ -361,6 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
                         acc[j] = __float_as_uint(__uint_as_float(acc[j]) + __uint_as_float(second[j]));
                 }
                 if (i + 1 < rounds) next.load(e, m_tile + column(i + 1), n);
+                __syncwarp();
                 tmem_wait_ld();
                 if (i == last_shared) {
                     tc_fence_before();
@@ -587,6 +591,7 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
 #pragma unroll
                 for (int j = 0; j < G::CHUNK; ++j) acc[j] = __float_as_uint(sum[j]);
             } else {
+                __syncwarp();   // as in the pair kernel
                 tmem_ld_cols<G::CHUNK>(taddr + c, acc);
                 tmem_wait_ld();
             }
@@ -594,6 +599,7 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
             cur = next;
         }
     }
+    __syncwarp();
     tc_fence_before();
     if constexpr (SPLIT > 1)
         cluster_sync();   // nobody leaves while its shared memory is being read

@@ -639,3 +639,19 @@ def test_refused_nvfp4_operands(cuda_dev):
         with pytest.raises(ValueError):
             nv.w4a4_gemm_fused(a, b)
     done()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 33, 64), (1, 129, 4096), (30, 131, 2048), (40, 161, 3200), (60, 97, 320), (100, 225, 2048), (100, 1, 8192),
+                                   (500, 33, 192), (2300, 2335, 192), (2300, 2305, 4160)])
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+def test_a_warp_partly_past_the_last_row(cuda_dev, M, N, K, out_dtype):
+    """N cuts a warp's 32 weight rows, in each kernel and split; bias, residual, activation."""
+    bias, r = torch.randn(N, generator=gen(101), device="cuda"), rand((M, N), 102, out_dtype, pad=1)
+    A, B = fp8_pair(M, N, K, 103)
+    C = nv.w8a8_gemm(A, B, bias=bias, act=nv.ACT_SILU, residual=r, out_dtype=out_dtype)
+    done()
+    check_product(C, value(A), value(B), 32, bias, nv.ACT_SILU, r)
+    A, B = nv.nvfp4_quantize(rand((M, K), 104)), nv.nvfp4_quantize(rand((N, K), 105, std=0.1))
+    C = nv.w4a4_gemm_fused(A, B, bias=bias, act=nv.ACT_SILU, residual=r, out_dtype=out_dtype)
+    done()
+    check_product(C, nvfp4_value(A), nvfp4_value(B), 64, bias, nv.ACT_SILU, r)
