@@ -412,6 +412,13 @@ typedef struct {
 NVFP4_API nvfp4_status w8a8_gemm(const fp8_tensor* A, const fp8_tensor* B, const gemm_epilogue* epilogue,
                                  nvfp4_stream_t stream);
 
+/* Test hook: w8a8_gemm for sizes whose K it splits over a cluster of CTAs (else
+ * NVFP4_ERR_UNSUPPORTED_SHAPE), in which the second CTA of each cluster copies no
+ * operand, so that its waits run out (about half a second).  Nothing is stored, the
+ * next nvfp4_check_device_error() reports NVFP4_ERR_TIMEOUT, the context stays usable. */
+NVFP4_API nvfp4_status nvfp4_selftest_split_expiry(const fp8_tensor* A, const fp8_tensor* B,
+                                                   const gemm_epilogue* epilogue, nvfp4_stream_t stream);
+
 /* w4a4_gemm's product (NVFP4 operands, see there) with the epilogue above.
  * Requirements: K % 64 == 0, A->cols == B->cols == K, M, N <= 2^30. */
 NVFP4_API nvfp4_status w4a4_gemm_fused(const nvfp4_tensor* A, const nvfp4_tensor* B, const gemm_epilogue* epilogue,

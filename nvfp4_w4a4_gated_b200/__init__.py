@@ -23,7 +23,7 @@ __all__ = [
     "NVFP4Error", "NVFP4Matrix", "GdnDims", "LayerWeights", "lib", "nvfp4_quantize", "w4a4_gemm", "gdn_gates",
     "gdn_scan", "gdn_scan_noalloc", "gdn_output_gate", "gdn_short_conv", "gdn_layer_forward", "layer_workspace_layout",
     "check_device_error", "gdn_scan_transition", "gdn_state_combine", "gdn_scan_correct", "gdn_scan_span",
-    "selftest_wait_timeout", "FORM_PAGES",
+    "selftest_wait_timeout", "selftest_split_expiry", "FORM_PAGES",
     "FORM_STANDARD", "SCAN_AUTO", "SCAN_RECURRENT", "SCAN_CHUNKED", "EXPORTED_SYMBOLS", "QUANT_COMPUTE_SCALE",
     "QUANT_GIVEN_SCALE", "QUANT_AMAX_ONLY", "QUANT_FROM_AMAX",
     "FP8Matrix", "fp8_quantize", "add_rmsnorm_quantize", "w8a8_gemm", "w4a4_gemm_fused", "ACT_NONE", "ACT_SILU",
@@ -45,6 +45,7 @@ EXPORTED_SYMBOLS = [
     "gdn_short_conv", "gdn_layer_forward_stateful", "gdn_scan_transition_workspace_size", "gdn_scan_transition",
     "gdn_state_combine", "gdn_scan_correct", "gdn_scan_span_workspace_size", "gdn_scan_span",
     "gdn_layer_forward_timed", "fp8_quantize", "add_rmsnorm_quantize", "w8a8_gemm", "w4a4_gemm_fused",
+    "nvfp4_selftest_split_expiry",
 ]
 
 
@@ -152,10 +153,12 @@ def lib() -> ctypes.CDLL:
         L.add_rmsnorm_quantize.argtypes = [P, i32, i64, P, i32, i64, P, ctypes.c_float, i64, i64, P, i64, FP, P, i64, P,
                                            P]
         L.w8a8_gemm.argtypes = [FP, FP, EP, P]
+        L.nvfp4_selftest_split_expiry.argtypes = [FP, FP, EP, P]
         L.w4a4_gemm_fused.argtypes = [TP, TP, EP, P]
         for f in ("nvfp4_check_device_error", "nvfp4_selftest_wait_timeout", "nvfp4_quantize", "w4a4_gemm", "gdn_gates", "gdn_scan",
                   "gdn_layer_workspace_layout", "gdn_layer_forward", "gdn_scan_noalloc", "gdn_layer_forward_timed",
-                  "fp8_quantize", "add_rmsnorm_quantize", "w8a8_gemm", "w4a4_gemm_fused"):
+                  "fp8_quantize", "add_rmsnorm_quantize", "w8a8_gemm", "w4a4_gemm_fused",
+                  "nvfp4_selftest_split_expiry"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -518,6 +521,15 @@ def w8a8_gemm(A: FP8Matrix, B: FP8Matrix, bias=None, act: int = ACT_NONE, residu
     a, b = A.c(), B.c(dev=dev)
     out, e = _epilogue(a.rows, b.rows, A.codes, dev, bias, act, residual, out, out_dtype, stream)
     _on(dev, stream, lib().w8a8_gemm, ctypes.byref(a), ctypes.byref(b), ctypes.byref(e))
+    return out
+
+
+def selftest_split_expiry(A: FP8Matrix, B: FP8Matrix, residual=None, out=None, stream=None) -> torch.Tensor:
+    """Exercise the expired wait of a w8a8_gemm with split K (see the C header)."""
+    dev = A.codes.get_device()
+    a, b = A.c(), B.c(dev=dev)
+    out, e = _epilogue(a.rows, b.rows, A.codes, dev, None, ACT_NONE, residual, out, torch.float32, stream)
+    _on(dev, stream, lib().nvfp4_selftest_split_expiry, ctypes.byref(a), ctypes.byref(b), ctypes.byref(e))
     return out
 
 

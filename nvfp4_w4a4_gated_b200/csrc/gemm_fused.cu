@@ -95,6 +95,7 @@ struct FusedArgs {
     int row_bytes;     // bytes of a row's K codes
     int tail_from;     // pair kernel: the tiles from this one on are cut into
     int tail_shift;    //   2^tail_shift narrow ones
+    int stalled_rank;  // split-K kernel: the CTA of each cluster that copies nothing (-1; self-test)
     unsigned int* err;
     EpiArgs epi;
 };
@@ -428,6 +429,10 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ void st_shared_cluster(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 template <bool kFp4, int BN, int SPLIT>
 __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
     fused_small_kernel(const __grid_constant__ Maps maps, const __grid_constant__ FusedArgs args) {
@@ -440,6 +445,7 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
     uint64_t* acc_full = empty + G::STAGES;
     uint64_t* drained = acc_full + 1;   // products in flight, after an expired wait
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
+    volatile uint32_t* expired = tmem_holder + 1;   // [4] by lane quarter: a CTA of the cluster has no sum to join
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     const int rank = SPLIT > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -458,6 +464,7 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
         mbar_init(acc_full, 1);
         mbar_init(drained, 1);
         fence_mbar_init();
+        for (int i = 0; i < 4; ++i) expired[i] = 0;
     }
     if (warp == 1) {
         tmem_alloc(tmem_holder, G::TMEM_COLS);
@@ -469,12 +476,14 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (SPLIT > 1) cluster_arrive();   // the others may write `expired`
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     pdl_wait_and_trigger();
 
     const int q = warp & 3;
-    int n = n_idx * 128 + q * 32 + lane;
+    const int n = n_idx * 128 + q * 32 + lane;
+    bool ok = true;   // this warp's sum is there, and those it joins
     const EpiArgs& e = args.epi;
     const int m_tile = m_idx * BN;
     const int chunk0 = G::CHUNKS * rank / SPLIT, chunk1 = G::CHUNKS * (rank + 1) / SPLIT;
@@ -485,7 +494,7 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
         if (elect_one()) {
             const int kb_total = args.row_bytes / kStepK;   // NVFP4: scale atoms along K
             int i = 0;
-            for (int kt = kt0; kt < kt1; ++kt, ++i) {
+            for (int kt = kt0; kt < kt1 && rank != args.stalled_rank; ++kt, ++i) {
                 const int stage = i % G::STAGES;
                 if (!mbar_wait(&empty[stage], ((i / G::STAGES) & 1) ^ 1, err, kErrTimeoutTma)) break;
                 mbar_arrive_expect_tx(&full[stage], G::STAGE_BYTES);
@@ -547,8 +556,7 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
         }
         cur.load(e, m_tile + chunk0 * G::CHUNK, n);
         if constexpr (!kFp4) stage_token_scales(args.sA, e.M, m_tile, BN, s, lane);
-        // expired: nothing is stored
-        if (!__all_sync(0xffffffffu, mbar_wait(acc_full, 0, err, kErrTimeoutEpi))) n = e.N;
+        ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, err, kErrTimeoutEpi));
         tc_fence_after();
     }
     __syncwarp();
@@ -556,10 +564,16 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
     const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
     if constexpr (SPLIT > 1) {
         // partial accumulators, [column][lane row]: the ring is free, its last product done
+        // (after an expired wait it may not be, and there is no sum: every CTA of the cluster is
+        // told, and none stores this quarter.  Asking all of them instead costs remote reads:
+        // one token x 5120 x 4096 5.3 and 5.6 us, without either 5.1)
         float* part = reinterpret_cast<float*>(smem);
+        cluster_wait();
         if (warp >= 2) {
+            if (!ok && lane < SPLIT) st_shared_cluster(mapa_shared(smem_u32(const_cast<uint32_t*>(expired + q)), lane), 1);
+            __syncwarp();
 #pragma unroll 1
-            for (int c = 0; c < BN; c += 16) {
+            for (int c = 0; ok && c < BN; c += 16) {
                 uint32_t acc[16];
                 tmem_ld_32x32b_x16(taddr + c, acc);
                 tmem_wait_ld();
@@ -568,6 +582,7 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
             }
         }
         cluster_sync();
+        if (warp >= 2) ok = expired[q] == 0;
     }
     if (warp >= 2) {
 #pragma unroll 1
@@ -595,7 +610,7 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
                 tmem_ld_cols<G::CHUNK>(taddr + c, acc);
                 tmem_wait_ld();
             }
-            epilogue_store<G::CHUNK, !kFp4>(e, m_tile + c, n, acc, cur, s + c, t, bias);
+            epilogue_store<G::CHUNK, !kFp4>(e, m_tile + c, ok ? n : e.N, acc, cur, s + c, t, bias);
             cur = next;
         }
     }
@@ -677,6 +692,7 @@ nvfp4_status launch_pair(const Operand& X, const Operand& W, const FusedArgs& ar
 template <bool kFp4, int BN, int SPLIT>
 nvfp4_status launch_small(const Operand& X, const Operand& W, const FusedArgs& args, cudaStream_t st) {
     using G = Small<kFp4, BN, SPLIT>;
+    if (args.stalled_rank >= SPLIT) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "K is not split for these sizes");
     Maps maps = {};
     nvfp4_status s = operand_maps(W, 128, &maps.w, &maps.sw);
     if (s == NVFP4_OK) s = operand_maps(X, BN, &maps.x, &maps.sx);
@@ -742,6 +758,7 @@ nvfp4_status fused_launch(const Operand& X, const Operand& W, const FusedArgs& a
     const int64_t pair_tiles = ((M + 255) / 256) * ((N + 255) / 256);
     const int64_t num_kt = (args.row_bytes + kTileK - 1) / kTileK;
     if (M > 128 && pair_tiles >= 32) {
+        if (args.stalled_rank >= 0) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "K is not split for these sizes");
         if constexpr (!kFp4)
             if (args.epi.out_dtype == NVFP4_DTYPE_FP32 && num_kt >= kChainTiles)
                 return launch_pair<false, true>(X, W, args, st);
@@ -800,6 +817,7 @@ nvfp4_status fused_args(const gemm_epilogue* e, int64_t M, int64_t N, FusedArgs*
     epi.out_dtype = e->out_dtype;
     epi.M = static_cast<int>(M);
     epi.N = static_cast<int>(N);
+    args->stalled_rank = -1;
     args->err = device_error_word();
     if (!args->err) return fail(NVFP4_ERR_CUDA, "device error word unavailable");
     return NVFP4_OK;
@@ -809,20 +827,32 @@ nvfp4_status fused_args(const gemm_epilogue* e, int64_t M, int64_t N, FusedArgs*
 
 }  // namespace nvg
 
-extern "C" nvfp4_status w8a8_gemm(const fp8_tensor* A, const fp8_tensor* B, const gemm_epilogue* epilogue,
-                                  nvfp4_stream_t stream) {
-    using namespace nvg;
+namespace nvg {
+static nvfp4_status w8a8_launch(const fp8_tensor* A, const fp8_tensor* B, const gemm_epilogue* epilogue, int stalled_rank,
+                                nvfp4_stream_t stream) {
     nvfp4_status s = validate_fp8(A, "A");
     if (s == NVFP4_OK) s = validate_fp8(B, "B");
     if (s != NVFP4_OK) return s;
     if (A->cols != B->cols) return fail(NVFP4_ERR_INVALID_ARG, "A and B have different K");
     FusedArgs args = {};
     if ((s = fused_args(epilogue, A->rows, B->rows, &args)) != NVFP4_OK) return s;
+    args.stalled_rank = stalled_rank;
     args.sA = A->scale;
     args.sB = B->scale;
     args.row_bytes = static_cast<int>(A->cols);
     const Operand x = {A->codes, nullptr, A->rows, A->cols, A->ld}, w = {B->codes, nullptr, B->rows, B->cols, B->ld};
     return fused_launch<false>(x, w, args, as_stream(stream));
+}
+}  // namespace nvg
+
+extern "C" nvfp4_status w8a8_gemm(const fp8_tensor* A, const fp8_tensor* B, const gemm_epilogue* epilogue,
+                                  nvfp4_stream_t stream) {
+    return nvg::w8a8_launch(A, B, epilogue, -1, stream);
+}
+
+extern "C" nvfp4_status nvfp4_selftest_split_expiry(const fp8_tensor* A, const fp8_tensor* B,
+                                                    const gemm_epilogue* epilogue, nvfp4_stream_t stream) {
+    return nvg::w8a8_launch(A, B, epilogue, 1, stream);
 }
 
 extern "C" nvfp4_status w4a4_gemm_fused(const nvfp4_tensor* A, const nvfp4_tensor* B, const gemm_epilogue* epilogue,
