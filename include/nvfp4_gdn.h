@@ -374,9 +374,11 @@ NVFP4_API nvfp4_status fp8_quantize(const void* x, int32_t x_dtype, int64_t rows
  *             into it with atomicMax on the float bits (it must hold a non-negative
  *             float, e.g. 0, beforehand).  As word 0 of nvfp4_quantize's workspace it
  *             lets NVFP4_QUANT_FROM_AMAX quantise norm_bf16 in one pass.
- * Matrices and pitches (times the element size) are 16-byte aligned.  A row whose mean
- * square, or whose largest |h w / sqrt(..)|, is not a finite float32 gets NaN
- * throughout.  Requirements as for fp8_quantize. */
+ * Matrices and pitches (times the element size) are 16-byte aligned.  A row whose sum
+ * of squares (not its mean: 5120 values of 2.6e17 are too many), largest |h w| or
+ * largest |n| is not a finite float32 gets NaN throughout (scale, codes, norm_bf16, and
+ * amax_word's bits are then those of a NaN); h is stored as it is.  Requirements as for
+ * fp8_quantize. */
 NVFP4_API nvfp4_status add_rmsnorm_quantize(const void* x, int32_t x_dtype, int64_t ld_x, const void* residual,
                                             int32_t residual_dtype, int64_t ld_residual, const float* w, float eps,
                                             int64_t rows, int64_t cols, void* h, int64_t ld_h, const fp8_tensor* out,

@@ -110,9 +110,11 @@ struct NoResidual {};   // TR when nothing is added
 // for the plain row quantiser; V values per vector, NV vectors per thread and row.
 // R = 0: a CTA per row.  R > 0: a warp takes R rows at a time, all their loads in
 // flight together.  T: most threads of a CTA; 384 and 512 keep registers for two CTAs an
-// SM, so that one works while the other waits for its row.
+// SM, so that one works while the other waits for its row; four rows a warp for five (65536 x
+// 128 fp32: 11.4 us, with four 12.3).
 template <typename TX, typename TR, bool kNorm, int V, int NV, int R, int T>
-__global__ void __launch_bounds__(T, T == 384 || T == 512 ? 2 : 0) row_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(T, T == 384 || T == 512 ? 2 : R == 4 && std::is_same<TR, NoResidual>::value ? 5 : 0)
+    row_kernel(const RowArgs a) {
     constexpr bool kAdd = !std::is_same<TR, NoResidual>::value;
     constexpr int N = R ? R : 1;
     using RT = typename std::conditional<kAdd, TR, float>::type;
@@ -236,14 +238,16 @@ __global__ void __launch_bounds__(T, T == 384 || T == 512 ? 2 : 0) row_kernel(co
         const int64_t row = row0 + k;
         float rstd = 1.0f;
         if constexpr (kNorm) {
-            const float ms = ss[k] / static_cast<float>(a.cols);
-            // a row whose mean square is not a finite fp32 number has no norm
-            rstd = ms <= 3.402823466e38f ? rsqrtf(ms + a.eps) : __uint_as_float(0x7FC00000u);
+            rstd = rsqrtf(ss[k] / static_cast<float>(a.cols) + a.eps);
         }
-        const float amax = kNorm ? __uint_as_float(top[k]) * rstd : __uint_as_float(top[k]);
+        // A row whose sum of squares, largest |h w| or largest |n| is not a finite fp32 number has no
+        // norm: NaN throughout.  (Summing scaled squares, so that the mean alone counts, takes 2 %
+        // longer, and 14 % with 4096 x 16384 bf16, for |h| over 1e17.)  0 ss is NaN for such a sum.
+        const float amax = kNorm ? fmaf(0.0f, ss[k], __fmul_rn(__uint_as_float(top[k]), rstd)) : __uint_as_float(top[k]);
+        const bool finite = amax <= 3.402823466e38f;
+        if (kNorm && !finite) rstd = __uint_as_float(0x7FC00000u);
         // NaN and infinity both give a NaN scale: the row decodes to NaN, not to numbers
-        const float S = amax < kAmaxFloor ? 1.0f : amax <= 3.402823466e38f ? __fdiv_rn(amax, kE4m3Max)
-                                                                           : __uint_as_float(0x7FC00000u);
+        const float S = amax < kAmaxFloor ? 1.0f : finite ? __fdiv_rn(amax, kE4m3Max) : __uint_as_float(0x7FC00000u);
         const float inv = __frcp_rn(S);
         if constexpr (kNorm) {
 #pragma unroll
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(T, T == 384 || T == 512 ? 2 : 0) row_kernel(co
                 if (a.amax && t == 0) {
                     // rounding keeps order: the largest bf16 |n| is the rounded largest |n|
                     const uint32_t b =
-                        __float_as_uint(round_to(amax, static_cast<const __nv_bfloat16*>(nullptr))) & 0x7FFFFFFFu;
+                        finite ? __float_as_uint(round_to(amax, static_cast<const __nv_bfloat16*>(nullptr))) : 0x7FC00000u;
                     if (b > *static_cast<volatile unsigned int*>(a.amax)) atomicMax(a.amax, b);
                 }
             }

@@ -655,3 +655,50 @@ def test_a_warp_partly_past_the_last_row(cuda_dev, M, N, K, out_dtype):
     C = nv.w4a4_gemm_fused(A, B, bias=bias, act=nv.ACT_SILU, residual=r, out_dtype=out_dtype)
     done()
     check_product(C, nvfp4_value(A), nvfp4_value(B), 64, bias, nv.ACT_SILU, r)
+
+
+@pytest.mark.parametrize("cols", [112, 512, 5120, 16400])
+def test_norm_rows_that_overflow_are_nan_throughout(cuda_dev, cols):
+    """An infinite or NaN weight, h w past float32, a sum of squares past float32, and
+    rows just short of it."""
+    x = rand((9, cols), 111)
+    x[1:] = 0.0
+    x[1, 3] = 1.0
+    x[2, 3], x[2, 5] = 1e-30, 1e18        # h w = 1e47 at 5
+    x[3] = math.sqrt(3.3e38 / cols)       # the sum of squares just fits
+    x[4] = math.sqrt(3.5e38 / cols)       # and just does not, while the mean does
+    x[5, 8] = 1.0                         # the infinity's column: 0 w too is NaN
+    w = torch.ones(cols, device="cuda")
+    w[5] = 1e29
+    x[0, 5], x[3, 5], x[4, 5] = 0.0, 0.0, 0.0
+    word = torch.zeros(1, device="cuda")
+    h, q, n = nv.add_rmsnorm_quantize(x, w, residual=torch.zeros_like(x), want_norm=True, amax_word=word)
+    done()
+    good, bad = [0, 1, 3, 5, 6, 7, 8], [2, 4]
+    assert torch.equal(h, x)
+    ref = norm_ref(h[good], w)
+    assert torch.all((n[good].double() - ref).abs() <= (2.0 ** -8 + 33 * U) * ref.abs() + 2.0 ** -133)
+    check_codes(nv.FP8Matrix(q.codes[good], q.scale[good]), ref)
+    assert torch.all(torch.isnan(q.scale[bad])) and torch.all(torch.isnan(q.codes[bad].float()))
+    assert torch.all(torch.isnan(n[bad].float())) and torch.all(torch.isnan(word))
+    for value in (math.inf, -math.inf, math.nan):
+        w[5] = value
+        _, q, n = nv.add_rmsnorm_quantize(x, w, want_norm=True)
+        done()
+        assert torch.all(torch.isnan(q.scale)) and torch.all(torch.isnan(q.codes.float())) and torch.all(torch.isnan(n.float()))
+    # a tiny mean square and a large weight: n = 1e-18 3e38 / sqrt(1e-36 + 1e-38) = 2.985e38 still fits
+    tiny = torch.full((2, cols), 1e-18, device="cuda")
+    w.fill_(1.0)
+    w[7] = 3e38
+    _, q, n = nv.add_rmsnorm_quantize(tiny, w, eps=1e-38, want_norm=True)
+    done()
+    ref = norm_ref(tiny, w, 1e-38)
+    assert torch.all((n.double() - ref).abs() <= (2.0 ** -8 + 33 * U) * ref.abs())
+    check_codes(q, ref)
+    # alone in its row it is sqrt(cols) times that, while h w = 3e20
+    tiny[1] = 0.0
+    tiny[1, 7] = 1e-18
+    _, q, n = nv.add_rmsnorm_quantize(tiny, w, eps=1e-38, want_norm=True)
+    done()
+    assert not torch.isnan(q.scale[0]) and torch.isnan(q.scale[1])
+    assert torch.all(torch.isnan(n[1].float())) and torch.all(torch.isnan(q.codes[1].float()))
