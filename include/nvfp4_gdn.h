@@ -408,6 +408,11 @@ typedef struct {
 
 /* p[m, n] = A->scale[m] B->scale[n] sum_k e4m3(A)[m, k] e4m3(B)[n, k], tensor-core
  * products accumulated in float32 (tcgen05 kind::f8f6f4), then the epilogue.
+ * The tensor cores' float32 sums do not round to nearest: measured on activations with
+ * hot channels, a chain of K values is off by 1.9e-10 K of the result's norm (one sign
+ * throughout: 4.4e-10 K).  For a float32 result K is summed in chains of at most 3840,
+ * joined with rounding to nearest: within 7.5e-7 of the norm at any K (one sign: 1.7e-6).
+ * For a bf16 result the chains have at most 65536 values.
  * A: [M x K] (activations), B: [N x K] (weights).  The result does not depend on
  * timing: no atomics, a fixed order of summation for given sizes.
  * Requirements: K % 16 == 0, A->cols == B->cols == K <= 2^24, M, N <= 2^30. */
@@ -421,7 +426,9 @@ NVFP4_API nvfp4_status w8a8_gemm(const fp8_tensor* A, const fp8_tensor* B, const
 NVFP4_API nvfp4_status nvfp4_selftest_split_expiry(const fp8_tensor* A, const fp8_tensor* B,
                                                    const gemm_epilogue* epilogue, nvfp4_stream_t stream);
 
-/* w4a4_gemm's product (NVFP4 operands, see there) with the epilogue above.
+/* w4a4_gemm's product (NVFP4 operands, see there) with the epilogue above.  One chain of
+ * float32 sums at any K; measured as above, off by 4.5e-8 of the norm at K = 5120, 7e-7 at
+ * 28672 (one sign: 2e-7, 6e-6).
  * Requirements: K % 64 == 0, A->cols == B->cols == K, M, N <= 2^30. */
 NVFP4_API nvfp4_status w4a4_gemm_fused(const nvfp4_tensor* A, const nvfp4_tensor* B, const gemm_epilogue* epilogue,
                                        nvfp4_stream_t stream);

@@ -95,6 +95,7 @@ struct FusedArgs {
     int row_bytes;     // bytes of a row's K codes
     int tail_from;     // pair kernel: the tiles from this one on are cut into
     int tail_shift;    //   2^tail_shift narrow ones
+    int chain_tiles;   // 8-bit, kernels with chains: k-tiles summed in one chain at most
     int stalled_rank;  // split-K kernel: the CTA of each cluster that copies nothing (-1; self-test)
     unsigned int* err;
     EpiArgs epi;
@@ -144,13 +145,32 @@ struct Pair {
 };
 static_assert(Pair<true>::SMEM <= 232448 && Pair<false>::SMEM <= 232448, "shared memory of one CTA");
 
-// kChains (8-bit): the second half of K's tiles goes to the second accumulator and the
-// epilogue adds the two, see fused_launch.
+// Sums of 8-bit products in several chains of k-tiles, see fused_launch.  The first chain goes
+// to one accumulator and each later one to another; the epilogue warps add the second to the
+// first, rounding to nearest, before the next chain begins, and the last chain as they read it.
+struct Chains {
+    int count, tiles;
+    // first tile after chain i
+    __device__ __forceinline__ int end(int i) const { return (tiles * (i + 1) + count - 1) / count; }
+};
+
+// C columns of both accumulators, added (rounded to nearest), in acc.
+template <int C>
+__device__ __forceinline__ void add_chain(uint32_t first, uint32_t second, uint32_t (&acc)[C]) {
+    uint32_t last[C];
+    tmem_ld_cols<C>(first, acc);
+    tmem_ld_cols<C>(second, last);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < C; ++j) acc[j] = __float_as_uint(__uint_as_float(acc[j]) + __uint_as_float(last[j]));
+}
+
+// kChains (8-bit): two or more chains, the first in the first accumulator.
 template <bool kFp4, bool kChains>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS, 1)
     fused_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ FusedArgs args) {
     using G = Pair<kFp4>;
-    static_assert(!(kFp4 && kChains), "two chains are for 8-bit operands");
+    static_assert(!(kFp4 && kChains), "chains are for 8-bit operands");
     // one accumulator signal per tile instead of one per buffer
     constexpr bool kOneSignal = kFp4 || kChains;
     extern __shared__ uint8_t smem_raw[];
@@ -158,6 +178,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
     float* scales = reinterpret_cast<float*>(smem + G::STAGES * G::STAGE_BYTES);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::STAGES * G::STAGE_BYTES + G::SCALES);   // even CTA's are used
     uint64_t* empty = full + G::STAGES;
+    // kChains: [0] for the tile, [1] for each join of chains
     uint64_t* acc_full = empty + G::STAGES;   // [2] by buffer
     uint64_t* acc_free = acc_full + 2;        // even CTA's are used; [2] by buffer, or one with a phase a tile (kOneSignal)
     uint64_t* drained = acc_free + 2;         // products in flight, after an expired wait
@@ -170,6 +191,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
     const int tail_from = args.tail_from, tail_shift = args.tail_shift;
     const int num_units = tail_from + ((num_m * num_n - tail_from) << tail_shift);
     const int num_kt = (args.row_bytes + kTileK - 1) / kTileK;
+    const Chains chains = {kChains ? max(2, (num_kt + args.chain_tiles - 1) / args.chain_tiles) : 1, num_kt};
     unsigned int* err = args.err;
     // Tiles run in bands of 16 token tiles, weight tiles slowest inside a band, so that the
     // tiles in flight share rows of both operands (8192 x 12352 x 5120 under a steady load:
@@ -262,16 +284,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
             // -------------------------------------------------- MMA (even CTA) --
             const uint32_t peer_acc_full = mapa_shared(smem_u32(acc_full), 1);
             const uint32_t peer_empty = mapa_shared(smem_u32(empty), 1);
-            uint32_t stage = 0, phase = 0;
+            uint32_t stage = 0, phase = 0, joins = 0;
             int local = 0;
             bool ok = true;
             for (int u = pair; u < num_units && ok; u += npairs, ++local) {
                 const int buf = kChains ? 0 : local & 1, shift = u < tail_from ? 0 : tail_shift;
-                const int second = kChains ? (num_kt + 1) / 2 : 0;   // the second chain's first tile
+                int chain = 0, chain_from = 0, chain_end = chains.end(0);
                 const uint32_t idesc = shift == 0 ? G::idesc(256) : shift == 1 ? G::idesc(128) : G::idesc(64);
                 // 8-bit: this buffer's last tile has been read.  NVFP4: the shared columns of the
                 // tile before have been; its readers had by then finished the tile before it.
-                // Two chains: all of the tile before has been read.
+                // Chains: all of the tile before has been read.
                 if (kOneSignal ? local >= 1 && !mbar_wait_cluster(acc_free, (local - 1) & 1, err, kErrTimeoutMma)
                          : local >= 2 && !mbar_wait_cluster(&acc_free[buf], ((local >> 1) - 1) & 1, err, kErrTimeoutMma)) {
                     ok = false;
@@ -279,6 +301,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
                 }
                 tc_fence_after();
                 for (int kt = 0; kt < num_kt; ++kt) {
+                    if (kChains && kt == chain_end) {
+                        if (chain) {
+                            // the second accumulator is added to the first, then free
+                            mma_commit_pair(smem_u32(&acc_full[1]));
+                            mma_commit_pair(peer_acc_full + 8);
+                            if (!mbar_wait_cluster(&acc_free[1], joins++ & 1, err, kErrTimeoutMma)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                        }
+                        chain_from = kt;
+                        chain_end = chains.end(++chain);
+                    }
                     if (!mbar_wait_cluster(&full[stage], phase, err, kErrTimeoutMma)) {
                         ok = false;
                         break;
@@ -286,10 +322,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
                     tc_fence_after();
                     const uint32_t a = smem_u32(smem + stage * G::STAGE_BYTES), b = a + G::A_BYTES;
                     const int nk = min(4, (args.row_bytes - kt * kTileK + kStepK - 1) / kStepK);
-                    const uint32_t acc = tmem + (kChains ? (kt >= second) * 256 : buf * G::ACC_OFF);
+                    const uint32_t acc = tmem + (kChains ? (chain > 0) * 256 : buf * G::ACC_OFF);
                     for (int j = 0; j < nk; ++j) {
                         const uint64_t da = sdesc_kmajor_sw128(a + j * kStepK), db = sdesc_kmajor_sw128(b + j * kStepK);
-                        const uint32_t accumulate = (j > 0 || (kt > 0 && !(kChains && kt == second))) ? 1u : 0u;
+                        const uint32_t accumulate = (j > 0 || kt > chain_from) ? 1u : 0u;
                         if constexpr (kFp4) {
                             const uint32_t sfa = tmem + G::SF_BASE + j * G::SF_STEP, sfb = sfa + 4;
                             const uint32_t src = b + G::B_BYTES + j * kAtomBytes;
@@ -325,6 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
         float* s = scales + (warp - 2) * G::EPI_COLS;
         const float whole = kFp4 ? __fmul_rn(*args.sA, *args.sB) : 0.0f;
         int local = 0;
+        uint32_t joins = 0;
         for (int u = pair; u < num_units; u += npairs, ++local) {
             const Unit w = unit_of(u);
             const int buf = kChains ? 0 : local & 1, m_tile = w.m0;
@@ -342,6 +379,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
             EpiResidual<16> cur, next;
             cur.load(e, m_tile + column(0), n);
             if constexpr (!kFp4) stage_token_scales(args.sA, e.M, m_tile + column(0), G::EPI_COLS, s, lane);
+            if constexpr (kChains) {
+                const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+                bool ok = true;
+                for (int c = 2; c < chains.count && ok; ++c) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_full[1], joins++ & 1, err, kErrTimeoutEpi));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int i = 0; i < rounds; ++i) {
+                        uint32_t acc[16];
+                        add_chain(taddr + column(i), taddr + 256 + column(i), acc);
+                        tmem_st_32x32b_x16(taddr + column(i), acc);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&acc_free[1]), 0));
+                    __syncwarp();
+                }
+                if (!ok) break;
+            }
             // the warp stays together whichever of its lanes saw the budget run out
             if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_full[buf], (kChains ? local : local >> 1) & 1, err, kErrTimeoutEpi))) break;
             tc_fence_after();
@@ -355,15 +413,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
                 // lanes past N take another path through the loads and stores of C and R, and
                 // TMEM instructions want the warp together
                 __syncwarp();
-                tmem_ld_32x32b_x16(taddr + c, acc);
-                if constexpr (kChains) {
-                    uint32_t second[16];
-                    tmem_ld_32x32b_x16(taddr + 256 + c, second);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        acc[j] = __float_as_uint(__uint_as_float(acc[j]) + __uint_as_float(second[j]));
-                }
+                if constexpr (kChains)
+                    add_chain(taddr + c, taddr + 256 + c, acc);
+                else
+                    tmem_ld_32x32b_x16(taddr + c, acc);
                 if (i + 1 < rounds) next.load(e, m_tile + column(i + 1), n);
                 __syncwarp();
                 tmem_wait_ld();
@@ -396,8 +449,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
 // meet in shared memory: each CTA leaves its own there and then adds, in rank order,
 // the token columns that are its share, read from every CTA of the cluster.
 // The order is fixed: no atomics, the same bits every time.
-template <bool kFp4, int BN, int SPLIT>
+// kChains (8-bit): a CTA's range of K in two or more chains.
+template <bool kFp4, int BN, int SPLIT, bool kChains>
 struct Small {
+    static_assert(!(kFp4 && kChains), "chains are for 8-bit operands");
     static constexpr int A_BYTES = 128 * kTileK;
     static constexpr int B_BYTES = BN * kTileK;
     static constexpr int SF_BYTES = kFp4 ? kAtoms * kAtomBytes : 0;   // of the weight rows, and of the tokens
@@ -416,7 +471,7 @@ struct Small {
     static constexpr int SMEM = RING + SCALES + 256 + 1024;
     static constexpr int ACC_COLS = BN < 32 ? 32 : BN;
     static constexpr int SF_STEP = 8;                                 // scale columns of a step: 4 for A, 4 for B
-    static constexpr int USED_COLS = ACC_COLS + (kFp4 ? kAtoms * SF_STEP : 0);
+    static constexpr int USED_COLS = ACC_COLS + (kFp4 ? kAtoms * SF_STEP : kChains ? ACC_COLS : 0);
     static constexpr int TMEM_COLS = USED_COLS <= 32 ? 32 : USED_COLS <= 64 ? 64 : USED_COLS <= 128 ? 128 : 256;
     static constexpr int THREADS = 192;
     static constexpr uint32_t IDESC = kFp4 ? idesc_nvf4(128, BN) : idesc_e4m3(128, BN);
@@ -433,10 +488,10 @@ __device__ __forceinline__ void st_shared_cluster(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-template <bool kFp4, int BN, int SPLIT>
-__global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
+template <bool kFp4, int BN, int SPLIT, bool kChains>
+__global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT, kChains>::CTAS)
     fused_small_kernel(const __grid_constant__ Maps maps, const __grid_constant__ FusedArgs args) {
-    using G = Small<kFp4, BN, SPLIT>;
+    using G = Small<kFp4, BN, SPLIT, kChains>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024_shared(smem_raw);
     float* scales = reinterpret_cast<float*>(smem + G::RING);
@@ -446,6 +501,8 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
     uint64_t* drained = acc_full + 1;   // products in flight, after an expired wait
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
     volatile uint32_t* expired = tmem_holder + 1;   // [4] by lane quarter: a CTA of the cluster has no sum to join
+    uint64_t* chain_full = reinterpret_cast<uint64_t*>(tmem_holder + 6);   // kChains: a chain to join,
+    uint64_t* chain_free = chain_full + 1;                                 //   its accumulator free again
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     const int rank = SPLIT > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -454,6 +511,7 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
     const int n_idx = tile / num_m, m_idx = tile - n_idx * num_m;
     const int num_kt = (args.row_bytes + kTileK - 1) / kTileK;
     const int kt0 = num_kt * rank / SPLIT, kt1 = num_kt * (rank + 1) / SPLIT;
+    const Chains chains = {kChains ? (kt1 - kt0 + args.chain_tiles - 1) / args.chain_tiles : 1, kt1 - kt0};
     unsigned int* err = args.err;
 
     if (threadIdx.x == 0) {
@@ -465,6 +523,11 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
         mbar_init(drained, 1);
         fence_mbar_init();
         for (int i = 0; i < 4; ++i) expired[i] = 0;
+        if (kChains) {
+            mbar_init(chain_full, 1);
+            mbar_init(chain_free, 4);
+            fence_mbar_init();
+        }
     }
     if (warp == 1) {
         tmem_alloc(tmem_holder, G::TMEM_COLS);
@@ -517,8 +580,22 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
     } else if (warp == 1) {
         if (elect_one()) {
             bool ok = true;
+            uint32_t joins = 0;
+            int chain = 0, chain_from = 0, chain_end = chains.end(0);
             for (int kt = kt0, i = 0; kt < kt1; ++kt, ++i) {
                 const int stage = i % G::STAGES;
+                if (kChains && i == chain_end) {
+                    if (chain) {
+                        mma_commit(chain_full);
+                        if (!mbar_wait(chain_free, joins++ & 1, err, kErrTimeoutMma)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
+                    chain_from = i;
+                    chain_end = chains.end(++chain);
+                }
                 if (!mbar_wait(&full[stage], (i / G::STAGES) & 1, err, kErrTimeoutMma)) {
                     ok = false;
                     break;
@@ -528,15 +605,16 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
                 const int nk = min(4, (args.row_bytes - kt * kTileK + kStepK - 1) / kStepK);
                 for (int j = 0; j < nk; ++j) {
                     const uint64_t da = sdesc_kmajor_sw128(a + j * kStepK), db = sdesc_kmajor_sw128(b + j * kStepK);
-                    const uint32_t accumulate = (i > 0 || j > 0) ? 1u : 0u;
+                    const uint32_t accumulate = (i > chain_from || j > 0) ? 1u : 0u;
+                    const uint32_t acc = kChains && chain ? tmem + G::ACC_COLS : tmem;
                     if constexpr (kFp4) {
                         const uint32_t sfa = tmem + G::ACC_COLS + j * G::SF_STEP, sfb = sfa + 4;
                         const uint32_t src = b + G::B_BYTES + j * kAtomBytes;
                         cp_scale_atom(sfa, sdesc_scale_atom(src));
                         cp_scale_atom(sfb, sdesc_scale_atom(src + G::SF_BYTES));
-                        mma_nvf4(tmem, da, db, G::IDESC, sfa, sfb, accumulate);
+                        mma_nvf4(acc, da, db, G::IDESC, sfa, sfb, accumulate);
                     } else {
-                        mma_fp8(tmem, da, db, G::IDESC, accumulate);
+                        mma_fp8(acc, da, db, G::IDESC, accumulate);
                     }
                 }
                 mma_commit(&empty[stage]);
@@ -556,7 +634,26 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
         }
         cur.load(e, m_tile + chunk0 * G::CHUNK, n);
         if constexpr (!kFp4) stage_token_scales(args.sA, e.M, m_tile, BN, s, lane);
-        ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, err, kErrTimeoutEpi));
+        if constexpr (kChains) {
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+            for (int c = 2; c < chains.count && ok; ++c) {
+                ok = __all_sync(0xffffffffu, mbar_wait(chain_full, c & 1, err, kErrTimeoutEpi));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int j = 0; j < BN; j += 16) {
+                    uint32_t acc[16];
+                    add_chain(taddr + j, taddr + G::ACC_COLS + j, acc);
+                    tmem_st_32x32b_x16(taddr + j, acc);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(chain_free);
+                __syncwarp();
+            }
+        }
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(acc_full, 0, err, kErrTimeoutEpi));
         tc_fence_after();
     }
     __syncwarp();
@@ -575,8 +672,12 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
 #pragma unroll 1
             for (int c = 0; ok && c < BN; c += 16) {
                 uint32_t acc[16];
-                tmem_ld_32x32b_x16(taddr + c, acc);
-                tmem_wait_ld();
+                if (kChains && chains.count > 1) {
+                    add_chain(taddr + c, taddr + G::ACC_COLS + c, acc);
+                } else {
+                    tmem_ld_32x32b_x16(taddr + c, acc);
+                    tmem_wait_ld();
+                }
 #pragma unroll
                 for (int j = 0; j < 16; ++j) part[(c + j) * 128 + q * 32 + lane] = __uint_as_float(acc[j]);
             }
@@ -607,8 +708,12 @@ __global__ void __launch_bounds__(192, Small<kFp4, BN, SPLIT>::CTAS)
                 for (int j = 0; j < G::CHUNK; ++j) acc[j] = __float_as_uint(sum[j]);
             } else {
                 __syncwarp();   // as in the pair kernel
-                tmem_ld_cols<G::CHUNK>(taddr + c, acc);
-                tmem_wait_ld();
+                if constexpr (kChains) {
+                    add_chain(taddr + c, taddr + G::ACC_COLS + c, acc);
+                } else {
+                    tmem_ld_cols<G::CHUNK>(taddr + c, acc);
+                    tmem_wait_ld();
+                }
             }
             epilogue_store<G::CHUNK, !kFp4>(e, m_tile + c, ok ? n : e.N, acc, cur, s + c, t, bias);
             cur = next;
@@ -689,16 +794,20 @@ nvfp4_status launch_pair(const Operand& X, const Operand& W, const FusedArgs& ar
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "fused pair launch");
 }
 
-template <bool kFp4, int BN, int SPLIT>
+template <bool kFp4, int BN, int SPLIT, bool kChains = false>
 nvfp4_status launch_small(const Operand& X, const Operand& W, const FusedArgs& args, cudaStream_t st) {
-    using G = Small<kFp4, BN, SPLIT>;
+    using G = Small<kFp4, BN, SPLIT, kChains>;
+    if constexpr (!kFp4 && !kChains) {
+        const int64_t num_kt = (args.row_bytes + kTileK - 1) / kTileK;
+        if ((num_kt + SPLIT - 1) / SPLIT > args.chain_tiles) return launch_small<kFp4, BN, SPLIT, true>(X, W, args, st);
+    }
     if (args.stalled_rank >= SPLIT) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "K is not split for these sizes");
     Maps maps = {};
     nvfp4_status s = operand_maps(W, 128, &maps.w, &maps.sw);
     if (s == NVFP4_OK) s = operand_maps(X, BN, &maps.x, &maps.sx);
     if (s != NVFP4_OK) return s;
     static PerDeviceOnce once;
-    if ((s = smem_limit_once(once, fused_small_kernel<kFp4, BN, SPLIT>, G::SMEM, "cudaFuncSetAttribute(fused small smem)")) !=
+    if ((s = smem_limit_once(once, fused_small_kernel<kFp4, BN, SPLIT, kChains>, G::SMEM, "cudaFuncSetAttribute(fused small smem)")) !=
         NVFP4_OK)
         return s;
     const int64_t tiles = ((X.rows + BN - 1) / BN) * ((W.rows + 127) / 128);
@@ -716,7 +825,7 @@ nvfp4_status launch_small(const Operand& X, const Operand& W, const FusedArgs& a
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = SPLIT > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fused_small_kernel<kFp4, BN, SPLIT>, maps, args);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fused_small_kernel<kFp4, BN, SPLIT, kChains>, maps, args);
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "fused small launch");
 }
 
@@ -729,17 +838,25 @@ nvfp4_status launch_split(int split, const Operand& X, const Operand& W, const F
     return split == 2 ? launch_small<kFp4, BN, 2>(X, W, args, st) : launch_small<kFp4, BN, 1>(X, W, args, st);
 }
 
-// k-tiles from which an 8-bit product with a float32 result is summed in at least two
-// chains.  The tensor cores' float32 accumulation does not round to nearest: against
-// float64 its error grows in proportion to the number of steps (K = 5120, 160 steps:
-// 9.6e-7 of the result's norm in one chain, 4.2e-7 in two, 1.9e-7 in four), and 30 tiles
-// (K = 3840) keep it under 7.5e-7.  A bf16 result's own rounding is 1.7e-3.  In the pair
-// kernel two chains cost the overlap of a tile's epilogue with the next tile's products
-// (8192 x 12352 x 5120 under a steady load: 494 us, one chain 467).  Leaving the first
-// chain's sum in the result instead keeps the overlap, but under the power limit the
-// extra traffic costs more (517); three stages and that sum in shared memory: three stages
-// alone take 20 % more.
+// k-tiles that an 8-bit product sums in one chain at most.  The tensor cores' float32
+// accumulation does not round to nearest: against float64 its error grows with the number of
+// steps (activations with hot channels, of the result's norm: K = 3712, one chain, 7.1e-7; 5120
+// 9.6e-7 in one, 4.4e-7 in two; 28672 3.7e-6 in two, 5.7e-7 in eight; operands of one sign about
+// 2.3 times that).  So a float32 result takes at least two chains from 30 tiles (K = 3840) on, of
+// at most 30 each, and stays within 7.5e-7 (one sign: 1.7e-6) at any K.  A bf16 result's own
+// rounding is 1.7e-3; 512 tiles, by the same growth (K^1.3), are near 3e-5.
+// In the pair kernel chains cost the overlap of a tile's epilogue with the next tile's products,
+// and from the third on a wait for the join (8192 x 12352 x 5120 fp32, two chains: 494 us where
+// one takes 467 on the same card; 2048 x 5120 x 17408, five: 150 and 145 us, under a steady load
+// 177 and 166, against two).  Leaving the first chain's sum in the result instead keeps the
+// overlap, but under the power limit the extra traffic costs more (517 against 494); three
+// stages and that sum in shared memory: three stages alone take 20 % more.  In the split-K
+// kernel they cost nothing to speak of (64 x 5120 x 17408: 21.7 and 21.8 us).
+// NVFP4 products take one chain: a step adds 64 products, and the error is 4.5e-8 at K = 5120,
+// 6.9e-7 at 28672 (one sign: 1.9e-7, 5.7e-6); 256 accumulator columns, their second copy and the
+// scales are more than TMEM has.
 constexpr int kChainTiles = 30;
+constexpr int kChainTilesBf16 = 512;
 
 // The pair kernel from 32 tiles of 256 x 256 on, when there are more than 128 tokens
 // (8-bit, 512 x 5120 x 4096, 40 tiles: 17.7 us against 19.9 for the best split; 256 x 5120
@@ -757,11 +874,11 @@ nvfp4_status fused_launch(const Operand& X, const Operand& W, const FusedArgs& a
     const int64_t M = X.rows, N = W.rows;
     const int64_t pair_tiles = ((M + 255) / 256) * ((N + 255) / 256);
     const int64_t num_kt = (args.row_bytes + kTileK - 1) / kTileK;
+    const bool wide = args.epi.out_dtype == NVFP4_DTYPE_FP32;
     if (M > 128 && pair_tiles >= 32) {
         if (args.stalled_rank >= 0) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "K is not split for these sizes");
         if constexpr (!kFp4)
-            if (args.epi.out_dtype == NVFP4_DTYPE_FP32 && num_kt >= kChainTiles)
-                return launch_pair<false, true>(X, W, args, st);
+            if (num_kt > args.chain_tiles || (wide && num_kt == kChainTiles)) return launch_pair<false, true>(X, W, args, st);
         return launch_pair<kFp4, false>(X, W, args, st);
     }
     const int64_t n_tiles = (N + 127) / 128, most = num_sms() * 3 / 2;
@@ -774,7 +891,7 @@ nvfp4_status fused_launch(const Operand& X, const Operand& W, const FusedArgs& a
     } else if (fits(3, num_sms())) {
         split = bn < 128 && fits(4, num_sms()) ? 4 : 3;
     }
-    if (!kFp4 && args.epi.out_dtype == NVFP4_DTYPE_FP32 && num_kt >= kChainTiles && split == 1) split = 2;
+    if (!kFp4 && wide && num_kt >= kChainTiles && split == 1) split = 2;
     if (bn == 16) return launch_split<kFp4, 16>(split, X, W, args, st);
     if (bn == 32) return launch_split<kFp4, 32>(split, X, W, args, st);
     if (bn == 64) return launch_split<kFp4, 64>(split, X, W, args, st);
@@ -818,6 +935,7 @@ nvfp4_status fused_args(const gemm_epilogue* e, int64_t M, int64_t N, FusedArgs*
     epi.M = static_cast<int>(M);
     epi.N = static_cast<int>(N);
     args->stalled_rank = -1;
+    args->chain_tiles = e->out_dtype == NVFP4_DTYPE_FP32 ? kChainTiles : kChainTilesBf16;
     args->err = device_error_word();
     if (!args->err) return fail(NVFP4_ERR_CUDA, "device error word unavailable");
     return NVFP4_OK;
