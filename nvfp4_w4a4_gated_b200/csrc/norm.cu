@@ -411,6 +411,7 @@ extern "C" nvfp4_status add_rmsnorm_quantize(const void* x, int32_t x_dtype, int
     if (!(eps > 0.0f) || !(eps <= 3.402823466e38f)) return fail(NVFP4_ERR_INVALID_ARG, "eps must be positive and finite");
     if (!out && !norm_bf16) return fail(NVFP4_ERR_INVALID_ARG, "neither out nor norm_bf16 is given");
     if (amax_word && !norm_bf16) return fail(NVFP4_ERR_INVALID_ARG, "amax_word needs norm_bf16");
+    if (reinterpret_cast<uintptr_t>(amax_word) % 4) return fail(NVFP4_ERR_MISALIGNED, "amax_word not 4-byte aligned");
     if ((residual == nullptr) != (h == nullptr))
         return fail(NVFP4_ERR_INVALID_ARG, "residual and h are given together or not at all");
     nvfp4_status s = check_size(rows, cols);

@@ -496,6 +496,8 @@ nvfp4_status validate_tensor(const nvfp4_tensor* t, const char* name) {
         return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, std::string(name) + " too large");
     if (!aligned16(t->codes) || !aligned16(t->sf))
         return fail(NVFP4_ERR_MISALIGNED, std::string(name) + " buffers must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(t->global_scale) % 4)
+        return fail(NVFP4_ERR_MISALIGNED, std::string(name) + " global_scale not 4-byte aligned");
     return NVFP4_OK;
 }
 

@@ -139,3 +139,12 @@ def test_nvfp4_buffers_that_do_not_hold_the_matrix(name, kw):
             call()
     with pytest.raises(ValueError, match="CUDA tensors"):
         good.c()
+
+
+def test_words_that_are_not_aligned():
+    """A kernel would read or update them as one 32-bit word."""
+    assert norm(n=FAKE + 64, amax=FAKE + 2) == 3
+    e = epilogue()
+    for a, b in ((FAKE + 2, FAKE), (FAKE, FAKE + 1)):
+        A, B = nv._Tensor(FAKE, FAKE, a, 8, 256), nv._Tensor(FAKE, FAKE, b, 64, 256)
+        assert nv.lib().w4a4_gemm_fused(ctypes.byref(A), ctypes.byref(B), ctypes.byref(e), None) == 3
