@@ -290,9 +290,12 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t saddr, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// The same without release semantics: for signals that only say that this thread's
-// TMEM reads are in registers.  A cluster-scope release first waits for all of the
-// thread's global stores.
+// The same without release semantics: for signals that only say that this warp's TMEM
+// reads are in registers.  What orders them before the arrival is tcgen05.wait::ld, after
+// which they are complete, then tcgen05.fence::before_thread_sync and, for the other lanes,
+// __syncwarp; the waiter acquires and issues tcgen05.fence::after_thread_sync before the
+// products that overwrite the columns.  Nothing in memory is handed over.  A cluster-scope
+// release first waits for all of the thread's global stores.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
