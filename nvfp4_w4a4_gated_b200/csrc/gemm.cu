@@ -21,8 +21,10 @@
 //               lane 32q + n%32, column base + n/32.  Each warp takes one lane
 //               quarter and tcgen05.st's those words from the staged atoms into
 //               one of two TMEM scale slots.
-//               tcgen05.cp would do the same through the tensor pipe, at a
-//               measured ~40 % of this kernel's time;
+//               tcgen05.cp does the same through the tensor pipe.  Issued
+//               behind `lane == 0` it took ~40 % of this kernel's time; the
+//               fused products (gemm_fused.cu) issue it behind elect.sync,
+//               where it is cheap.  Not measured here in that form;
 //   warps 2..5  epilogue: tcgen05.ld of the f32 accumulator (warp w reads
 //               TMEM lanes 32*(w%4)...), scale by S_A*S_B, write 32 x 32
 //               sub-tiles to shared memory (128-byte swizzle) and TMA-store

@@ -194,8 +194,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<kFp4>::THREADS,
     const Chains chains = {kChains ? max(2, (num_kt + args.chain_tiles - 1) / args.chain_tiles) : 1, num_kt};
     unsigned int* err = args.err;
     // Tiles run in bands of 16 token tiles, weight tiles slowest inside a band, so that the
-    // tiles in flight share rows of both operands (8192 x 12352 x 5120 under a steady load:
-    // bands of 4, 8, 16, 32 take 484, 471, 464, 472 us).
+    // tiles in flight share rows of both operands (8192 x 12352 x 5120 fp32 under a steady load:
+    // bands of 4, 8, 16, 32 take 484, 471, 464, 472 us; on another card 8 and 16 take 486, 479).
     struct Unit {
         int m0, n_idx, shift;   // first token, weight tile, 256 >> shift tokens
     };
@@ -846,12 +846,12 @@ nvfp4_status launch_split(int split, const Operand& X, const Operand& W, const F
 // at most 30 each, and stays within 7.5e-7 (one sign: 1.7e-6) at any K.  A bf16 result's own
 // rounding is 1.7e-3; 512 tiles, by the same growth (K^1.3), are near 3e-5.
 // In the pair kernel chains cost the overlap of a tile's epilogue with the next tile's products,
-// and from the third on a wait for the join (8192 x 12352 x 5120 fp32, two chains: 494 us where
-// one takes 467 on the same card; 2048 x 5120 x 17408, five: 150 and 145 us, under a steady load
-// 177 and 166, against two).  Leaving the first chain's sum in the result instead keeps the
-// overlap, but under the power limit the extra traffic costs more (517 against 494); three
-// stages and that sum in shared memory: three stages alone take 20 % more.  In the split-K
-// kernel they cost nothing to speak of (64 x 5120 x 17408: 21.7 and 21.8 us).
+// and from the third on a wait for the join (8192 x 12352 x 5120 fp32 under a steady load: 479 us
+// in two, 447 in one; 2048 x 5120 x 17408: 177 in five, 166 in two).  Leaving the first chain's
+// sum in the result instead keeps the overlap, but under the power limit the extra traffic
+// costs more (5 %); three stages and that sum in shared memory: three stages alone take 20 %
+// more.  In the split-K kernel chains cost little (64 x 5120 x 17408: 21.8 us in two a CTA, 21.7
+// in one).
 // NVFP4 products take one chain: a step adds 64 products, and the error is 4.5e-8 at K = 5120,
 // 6.9e-7 at 28672 (one sign: 1.9e-7, 5.7e-6); 256 accumulator columns, their second copy and the
 // scales are more than TMEM has.
@@ -859,16 +859,16 @@ constexpr int kChainTiles = 30;
 constexpr int kChainTilesBf16 = 512;
 
 // The pair kernel from 32 tiles of 256 x 256 on, when there are more than 128 tokens
-// (8-bit, 512 x 5120 x 4096, 40 tiles: 17.7 us against 19.9 for the best split; 256 x 5120
-// x 4096, 20 tiles: 16.0 against 14.6).  Below that the split-K kernel: the narrowest
+// (8-bit, 512 x 5120 x 4096, 40 tiles: 15.9 us against 17.2 for the best split; 256 x 5120
+// x 4096, 20 tiles: 13.0 against 12.3).  Below that the split-K kernel: the narrowest
 // token tile that holds the tokens (an NVFP4 tile has to begin a 128-row scale block, so
 // more than 128 tokens take tiles of 128).  K is split, four k-tiles at least each:
 //   up to 32 tokens, in 2 or 4 while the CTAs stay within 1.5 per SM (one token x 5120 x
-//     4096, 8-bit: 5.4 us in 4, 5.7 in 3, 6.9 in 2);
+//     4096, 8-bit: 5.3 us in 4, 6.5 in 2, 10.8 whole);
 //   above, in as many of at most 4 (3 for 128 tokens) as leave one CTA per SM, because the
-//     joining moves 32 or 64 KB a CTA (64 x 5120 x 4096: 7.3 us in 3, 8.0 in 4, 8.9 in 2;
-//     128 x 5120 x 4096: 9.1 in 3, 10.9 in 2), else in 2 within 1.5 per SM (64 x 12352 x
-//     5120: 15.5 in 2, 17.8 whole; in 3 the clusters no longer fit at once, 21).
+//     joining moves 32 or 64 KB a CTA (64 x 5120 x 4096: 7.0 us in 3, 8.0 in 4, 8.2 in 2;
+//     128 x 5120 x 4096: 8.8 in 3, 10.2 in 2), else in 2 within 1.5 per SM (64 x 12352 x
+//     5120: 15.4 in 2, 17.9 whole; in 3 the clusters no longer fit at once, 22).
 template <bool kFp4>
 nvfp4_status fused_launch(const Operand& X, const Operand& W, const FusedArgs& args, cudaStream_t st) {
     const int64_t M = X.rows, N = W.rows;

@@ -305,7 +305,7 @@ cudaError_t warp_rows_launch(const RowArgs& a, cudaStream_t st) {
 // x 5120: 30.2 and 29.4).  Rows over 6144 are kept to two CTAs an SM (4096 x 8192, fp32 x:
 // 60 and 54 us; rows of 5120 lose by it, 30.0 and 33.4).  Rows over 8192 take 32 values, in
 // CTAs of at most 384 or 512 threads (4096 x 12288, fp32 x, bf16 residual: 102 us in one
-// CTA of 768 threads, 91 in two of 384; 4096 x 16384 bf16: 118 and 102).
+// CTA of 768 threads, 91 in two of 384; 4096 x 16384 bf16 with a bf16 n: 118 and 100).
 template <typename TX, typename TR, bool kNorm>
 cudaError_t row_launch(const RowArgs& a, cudaStream_t st) {
     if (a.cols <= 128) return warp_rows_launch<TX, TR, kNorm, 1, 4>(a, st);
