@@ -289,9 +289,10 @@ class NVFP4Matrix:
                            torch.empty(1, dtype=torch.float32, device=device), rows, cols)
 
     def c(self, dev=None) -> _Tensor:
-        """The C form, after a check that the buffers hold a matrix of this size (on device ``dev``)."""
+        """The C form, after a check that the buffers hold a matrix of this size (on device
+        ``dev``); they may hold more, as buffers made for the most rows do."""
         codes, sf, scale, rows, cols = self.codes, self.sf, self.scale, self.rows, self.cols
-        if codes.nbytes * 2 != rows * cols or not codes.is_contiguous():
+        if codes.numel() * 2 < rows * cols or codes.element_size() != 1 or not codes.is_contiguous():
             raise ValueError(f"codes: {rows} x {cols // 2} contiguous bytes are expected")
         if sf.nbytes < (rows + 127) // 128 * 128 * (cols // 16) or not sf.is_contiguous():
             raise ValueError("sf: nvfp4_sf_bytes(rows, cols) contiguous bytes are expected")

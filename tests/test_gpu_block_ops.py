@@ -702,3 +702,14 @@ def test_norm_rows_that_overflow_are_nan_throughout(cuda_dev, cols):
     done()
     assert not torch.isnan(q.scale[0]) and torch.isnan(q.scale[1])
     assert torch.all(torch.isnan(n[1].float())) and torch.all(torch.isnan(q.codes[1].float()))
+
+
+def test_nvfp4_buffers_made_for_more_rows(cuda_dev):
+    """The first rows of larger buffers are a matrix of their own."""
+    x, B = rand((70, 256), 106), nv.nvfp4_quantize(rand((300, 256), 107))
+    large = nv.NVFP4Matrix.empty(500, 256)
+    some = dataclasses.replace(large, rows=70)
+    nv.nvfp4_quantize(x, out=some)
+    C, want = nv.w4a4_gemm_fused(some, B), nv.w4a4_gemm_fused(nv.nvfp4_quantize(x), B)
+    done()
+    assert torch.equal(C, want)
