@@ -5,6 +5,9 @@ Argument marshalling only: every step runs in the CUDA kernels of
 names mirror the C ABI in ``include/nvfp4_gdn.h``.  There is no CPU or PyTorch
 fallback: if the library is missing, importing the binding's entry points
 raises.  PyTorch is used only to own device memory and to name the stream.
+A call with ``stream=`` runs there and makes its new tensors there; that its
+inputs are ready on that stream, and stay alive until it has read them, is the
+caller's to see to, as is waiting for the stream before the results are read.
 """
 from __future__ import annotations
 
