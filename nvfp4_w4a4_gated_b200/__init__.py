@@ -17,6 +17,7 @@ import dataclasses
 import math
 import os
 import re
+import struct
 
 import torch
 
@@ -107,6 +108,12 @@ class _Epilogue(ctypes.Structure):
                 ("out_dtype", ctypes.c_int32), ("ldc", ctypes.c_int64)]
 
 
+# The same structures as bytes, which ctypes takes for a pointer: the block operators' small
+# calls last a few microseconds, and a Structure takes 0.3 to 0.5 of one to fill.
+_pack_tensor = struct.Struct("@PPPqq").pack
+_pack_fp8 = struct.Struct("@PPqqq").pack
+_pack_epilogue = struct.Struct("@PiPiqPiq").pack
+
 _lib = None
 
 
@@ -151,13 +158,12 @@ def lib() -> ctypes.CDLL:
         L.gdn_scan_span_workspace_size.restype = sz
         L.gdn_scan_span.argtypes = [P, P, P, i64, P, P, i32, i64, DP, ctypes.c_float, i32, i32, P, P, P, P, P, sz, P]
         L.gdn_scan_correct.argtypes = [P, P, P, i32, i64, i32, i32, i32, P, P]
-        FP, EP = ctypes.POINTER(_Fp8), ctypes.POINTER(_Epilogue)
-        L.fp8_quantize.argtypes = [P, i32, i64, i64, i64, FP, P]
-        L.add_rmsnorm_quantize.argtypes = [P, i32, i64, P, i32, i64, P, ctypes.c_float, i64, i64, P, i64, FP, P, i64, P,
+        L.fp8_quantize.argtypes = [P, i32, i64, i64, i64, P, P]
+        L.add_rmsnorm_quantize.argtypes = [P, i32, i64, P, i32, i64, P, ctypes.c_float, i64, i64, P, i64, P, P, i64, P,
                                            P]
-        L.w8a8_gemm.argtypes = [FP, FP, EP, P]
-        L.nvfp4_selftest_split_expiry.argtypes = [FP, FP, EP, P]
-        L.w4a4_gemm_fused.argtypes = [TP, TP, EP, P]
+        L.w8a8_gemm.argtypes = [P, P, P, P]
+        L.nvfp4_selftest_split_expiry.argtypes = [P, P, P, P]
+        L.w4a4_gemm_fused.argtypes = [P, P, P, P]
         for f in ("nvfp4_check_device_error", "nvfp4_selftest_wait_timeout", "nvfp4_quantize", "w4a4_gemm", "gdn_gates", "gdn_scan",
                   "gdn_layer_workspace_layout", "gdn_layer_forward", "gdn_scan_noalloc", "gdn_layer_forward_timed",
                   "fp8_quantize", "add_rmsnorm_quantize", "w8a8_gemm", "w4a4_gemm_fused",
@@ -291,9 +297,9 @@ class NVFP4Matrix:
                            torch.empty(sf_bytes, dtype=torch.uint8, device=device),
                            torch.empty(1, dtype=torch.float32, device=device), rows, cols)
 
-    def c(self, dev=None) -> _Tensor:
-        """The C form, after a check that the buffers hold a matrix of this size (on device
-        ``dev``); they may hold more, as buffers made for the most rows do."""
+    def fields(self, dev=None):
+        """The C form's fields, after a check that the buffers hold a matrix of this size (on
+        device ``dev``); they may hold more, as buffers made for the most rows do."""
         codes, sf, scale, rows, cols = self.codes, self.sf, self.scale, self.rows, self.cols
         if codes.numel() * 2 < rows * cols or codes.element_size() != 1 or not codes.is_contiguous():
             raise ValueError(f"codes: {rows} x {cols // 2} contiguous bytes are expected")
@@ -307,7 +313,10 @@ class NVFP4Matrix:
         if sf.get_device() != at or scale.get_device() != at or (dev is not None and at != dev):
             raise ValueError(f"codes, sf and scale are on {codes.device}, {sf.device} and {scale.device}, expected "
                              f"cuda:{at if dev is None else dev}")
-        return _Tensor(codes.data_ptr(), sf.data_ptr(), scale.data_ptr(), rows, cols)
+        return codes.data_ptr(), sf.data_ptr(), scale.data_ptr(), rows, cols
+
+    def c(self) -> _Tensor:
+        return _Tensor(*self.fields())
 
 
 @dataclasses.dataclass
@@ -321,9 +330,13 @@ class FP8Matrix:
         return FP8Matrix(torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device),
                          torch.empty(rows, dtype=torch.float32, device=device))
 
-    def c(self, shape=None, dev=None) -> _Fp8:
+    def fields(self, shape=None, dev=None):
+        """The C form's fields, after a check of the tensors."""
         ptr, rows, cols, ld, _, at = _rows(self.codes, "codes", _FP8, shape, dev)
-        return _Fp8(ptr, _vector(self.scale, "scale", rows, at), rows, cols, ld)
+        return ptr, _vector(self.scale, "scale", rows, at), rows, cols, ld
+
+    def c(self, shape=None, dev=None) -> _Fp8:
+        return _Fp8(*self.fields(shape, dev))
 
 
 @dataclasses.dataclass(frozen=True)
@@ -433,7 +446,7 @@ def _new_fp8(x, like, stream):
     else:
         codes = _made(stream, torch.empty, (rows, cols), dtype=torch.float8_e4m3fn, device=x.device)
         scale = _made(stream, torch.empty, rows, dtype=torch.float32, device=x.device)
-    return FP8Matrix(codes, scale), _Fp8(codes.data_ptr(), scale.data_ptr(), rows, cols, cols)
+    return FP8Matrix(codes, scale), _pack_fp8(codes.data_ptr(), scale.data_ptr(), rows, cols, cols)
 
 
 def fp8_quantize(x: torch.Tensor, out: FP8Matrix | None = None, stream=None) -> FP8Matrix:
@@ -442,8 +455,8 @@ def fp8_quantize(x: torch.Tensor, out: FP8Matrix | None = None, stream=None) -> 
     if out is None:
         out, q = _new_fp8(x, x, stream)
     else:
-        q = out.c(x.shape, dev)
-    _on(dev, stream, lib().fp8_quantize, ptr, dtype, rows, cols, ld, ctypes.byref(q))
+        q = _pack_fp8(*out.fields(x.shape, dev))
+    _on(dev, stream, lib().fp8_quantize, ptr, dtype, rows, cols, ld, q)
     return out
 
 
@@ -475,10 +488,9 @@ def add_rmsnorm_quantize(x: torch.Tensor, w: torch.Tensor, residual: torch.Tenso
     elif h is not None:
         raise ValueError("h is written only with a residual")
     if out is not None:
-        q = ctypes.byref(out.c(shape, dev))
+        q = _pack_fp8(*out.fields(shape, dev))
     elif want_fp8:
         out, q = _new_fp8(x, w, stream)
-        q = ctypes.byref(q)
     if norm is not None:
         n_ptr, _, _, n_ld, n_dtype, _ = _rows(norm, "norm", _DTYPES, shape, dev)
         if n_dtype != DTYPE_BF16:
@@ -509,11 +521,11 @@ def _epilogue(M: int, N: int, like, dev: int, bias, act: int, residual, out, out
         o_ptr, ldc = out.data_ptr(), N
     else:
         o_ptr, _, _, ldc, o_dtype, _ = _rows(out, "out", _DTYPES, shape, dev)
-    r_ptr, r_dtype, r_ld = None, 0, 0
+    r_ptr = r_dtype = r_ld = 0
     if residual is not None:
         r_ptr, _, _, r_ld, r_dtype, _ = _rows(residual, "residual", _DTYPES, shape, dev)
-    return out, _Epilogue(None if bias is None else _vector(bias, "bias", N, dev), act, r_ptr, r_dtype, r_ld, o_ptr,
-                          o_dtype, ldc)
+    return out, _pack_epilogue(0 if bias is None else _vector(bias, "bias", N, dev), act, r_ptr, r_dtype, r_ld, o_ptr,
+                               o_dtype, ldc)
 
 
 def w8a8_gemm(A: FP8Matrix, B: FP8Matrix, bias=None, act: int = ACT_NONE, residual=None, out=None,
@@ -522,18 +534,18 @@ def w8a8_gemm(A: FP8Matrix, B: FP8Matrix, bias=None, act: int = ACT_NONE, residu
     activations, B [N, K] weights, bias float32 [N], residual bf16 or fp32 [M, N].
     out (bf16 or fp32 [M, N]; a new tensor of out_dtype unless given) may be residual."""
     dev = A.codes.get_device()
-    a, b = A.c(), B.c(dev=dev)
-    out, e = _epilogue(a.rows, b.rows, A.codes, dev, bias, act, residual, out, out_dtype, stream)
-    _on(dev, stream, lib().w8a8_gemm, ctypes.byref(a), ctypes.byref(b), ctypes.byref(e))
+    a, b = A.fields(), B.fields(dev=dev)
+    out, e = _epilogue(a[2], b[2], A.codes, dev, bias, act, residual, out, out_dtype, stream)
+    _on(dev, stream, lib().w8a8_gemm, _pack_fp8(*a), _pack_fp8(*b), e)
     return out
 
 
 def selftest_split_expiry(A: FP8Matrix, B: FP8Matrix, residual=None, out=None, stream=None) -> torch.Tensor:
     """Exercise the expired wait of a w8a8_gemm with split K (see the C header)."""
     dev = A.codes.get_device()
-    a, b = A.c(), B.c(dev=dev)
-    out, e = _epilogue(a.rows, b.rows, A.codes, dev, None, ACT_NONE, residual, out, torch.float32, stream)
-    _on(dev, stream, lib().nvfp4_selftest_split_expiry, ctypes.byref(a), ctypes.byref(b), ctypes.byref(e))
+    a, b = A.fields(), B.fields(dev=dev)
+    out, e = _epilogue(a[2], b[2], A.codes, dev, None, ACT_NONE, residual, out, torch.float32, stream)
+    _on(dev, stream, lib().nvfp4_selftest_split_expiry, _pack_fp8(*a), _pack_fp8(*b), e)
     return out
 
 
@@ -541,9 +553,9 @@ def w4a4_gemm_fused(A: NVFP4Matrix, B: NVFP4Matrix, bias=None, act: int = ACT_NO
                     out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """act(A @ B^T + bias) + residual for NVFP4 operands; arguments as for w8a8_gemm."""
     dev = A.codes.get_device()
-    a, b = A.c(), B.c(dev)
+    a, b = A.fields(), B.fields(dev)
     out, e = _epilogue(A.rows, B.rows, A.codes, dev, bias, act, residual, out, out_dtype, stream)
-    _on(dev, stream, lib().w4a4_gemm_fused, ctypes.byref(a), ctypes.byref(b), ctypes.byref(e))
+    _on(dev, stream, lib().w4a4_gemm_fused, _pack_tensor(*a), _pack_tensor(*b), e)
     return out
 
 

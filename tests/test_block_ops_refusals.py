@@ -148,3 +148,10 @@ def test_words_that_are_not_aligned():
     for a, b in ((FAKE + 2, FAKE), (FAKE, FAKE + 1)):
         A, B = nv._Tensor(FAKE, FAKE, a, 8, 256), nv._Tensor(FAKE, FAKE, b, 64, 256)
         assert nv.lib().w4a4_gemm_fused(ctypes.byref(A), ctypes.byref(B), ctypes.byref(e), None) == 3
+
+
+def test_packed_structures_have_the_c_layout():
+    for struct_type, pack, values in ((nv._Tensor, nv._pack_tensor, (1 << 40, 2 << 40, 3 << 40, 64, 5120)),
+                                      (nv._Fp8, nv._pack_fp8, (1 << 40, 2 << 40, 64, 5120, 5136)),
+                                      (nv._Epilogue, nv._pack_epilogue, (1 << 40, 3, 2 << 40, 1, 77, 3 << 40, 1, 99))):
+        assert bytes(struct_type(*values)) == pack(*values)
